@@ -293,6 +293,50 @@ epx_status combine_impl(const epx_problem *p, const epx_layout *layout, int grou
                                               carry, out, s));
 }
 
+// The router's arguments besides its outputs.
+epx_status check_route(const Geometry &g, const void *logits, int32_t dtype, int32_t score,
+                       int32_t renormalize, float scale)
+{
+    if ((dtype != EPX_BF16 && dtype != EPX_F32) ||
+        (score != EPX_SCORE_SOFTMAX && score != EPX_SCORE_SIGMOID) ||
+        (renormalize != 0 && renormalize != 1) || !(scale - scale == 0.0f))
+        return EPX_ERR_ARG;
+    return g.T > 0 && (!logits || !aligned(logits, 16)) ? EPX_ERR_ARG : EPX_OK;
+}
+
+// The experts' row ranges; `viol` is set by arm_rows.
+epx_status make_rows(const epx_expert_rows *r, epx::ExpertRows *out)
+{
+    if (!r || r->num_experts < 1 || r->num_experts > epx::kMaxExperts || r->num_rows < 0)
+        return EPX_ERR_ARG;
+    if (!r->row_offset || !r->row_count || !aligned(r->row_offset, 4) || !aligned(r->row_count, 4))
+        return EPX_ERR_ARG;
+    out->offset = r->row_offset;
+    out->count = r->row_count;
+    out->n = r->num_experts;
+    out->num_rows = r->num_rows;
+    out->viol = nullptr;
+    return EPX_OK;
+}
+
+epx_status arm_rows(epx::ExpertRows &r)
+{
+    if (!epx::kChecked)
+        return EPX_OK;
+    return violations_on_current_device(&r.viol);
+}
+
+// Sizes of one expert's matrix of `rows` x inner: byte offsets into it and
+// into a tile's rows stay below 2^31.
+bool product_sizes_ok(int64_t rows, int32_t width, int32_t inner, int32_t unit_inner)
+{
+    constexpr int32_t kMost = 1 << 20;
+    return width >= 8 && width % 8 == 0 && width <= kMost && inner >= unit_inner &&
+           inner % unit_inner == 0 && inner <= kMost && rows * inner <= ((int64_t)1 << 30);
+}
+
+bool ready(const void *p, uintptr_t a) { return p && aligned(p, a); }
+
 }  // namespace
 
 extern "C" {
@@ -603,6 +647,199 @@ epx_status epx_f32_to_e4m3(const float *in, uint8_t *out, int64_t n, void *strea
     if (n == 0)
         return EPX_OK;
     return from_hip(epx::launch_f32_to_e4m3(in, out, n, (hipStream_t)stream));
+}
+
+epx_status epx_route(const epx_problem *p, const void *logits, int32_t logits_dtype, int32_t score,
+                     const float *bias, int32_t renormalize, float scale, int32_t *topk_idx,
+                     float *topk_weights, void *stream)
+{
+    HookScope hook_scope;
+    Geometry g;
+    epx_status st = make_geometry(p, &g);
+    if (st != EPX_OK)
+        return st;
+    if ((st = check_route(g, logits, logits_dtype, score, renormalize, scale)) != EPX_OK)
+        return st;
+    if (bias && (score != EPX_SCORE_SIGMOID || !aligned(bias, 4)))
+        return EPX_ERR_ARG;
+    if (g.T == 0)
+        return EPX_OK;
+    if (!ready(topk_idx, 4) || !ready(topk_weights, 4))
+        return EPX_ERR_ARG;
+    return from_hip(epx::launch_route(g, logits, logits_dtype == EPX_BF16,
+                                      score == EPX_SCORE_SOFTMAX, bias, renormalize != 0, scale,
+                                      topk_idx, topk_weights, (hipStream_t)stream));
+}
+
+epx_status epx_route_backward(const epx_problem *p, const void *logits, int32_t logits_dtype,
+                              int32_t score, int32_t renormalize, float scale,
+                              const int32_t *topk_idx, const float *dweights, void *dlogits,
+                              void *stream)
+{
+    HookScope hook_scope;
+    Geometry g;
+    epx_status st = make_geometry(p, &g);
+    if (st != EPX_OK)
+        return st;
+    if ((st = check_route(g, logits, logits_dtype, score, renormalize, scale)) != EPX_OK)
+        return st;
+    if (g.T == 0)
+        return EPX_OK;
+    if (!ready(topk_idx, 4) || !ready(dweights, 4) || !ready(dlogits, 16) || dlogits == logits)
+        return EPX_ERR_ARG;
+    return from_hip(epx::launch_route_backward(g, logits, logits_dtype == EPX_BF16,
+                                               score == EPX_SCORE_SOFTMAX, renormalize != 0, scale,
+                                               topk_idx, dweights, dlogits, (hipStream_t)stream));
+}
+
+epx_status epx_combine_backward(const epx_problem *p, const epx_layout *layout, const void *dout,
+                                const void *y, int64_t y_rows, const float *topk_weights,
+                                int32_t hidden, void *dy, float *dweights, void *stream)
+{
+    HookScope hook_scope;
+    Geometry g;
+    epx_status st = make_geometry(p, &g);
+    if (st != EPX_OK)
+        return st;
+    if ((st = check_layout(g, layout)) != EPX_OK)
+        return st;
+    if (hidden < 8 || hidden % 8 != 0)
+        return EPX_ERR_ARG;
+    if (y_rows < (int64_t)g.T * g.k)
+        return EPX_ERR_CAPACITY;
+    if (g.T == 0)
+        return EPX_OK;
+    if (!ready(dout, 16) || !ready(dy, 16) || !ready(topk_weights, 4) || dy == y || dy == dout)
+        return EPX_ERR_ARG;
+    if (dweights && (!ready(y, 16) || !aligned(dweights, 4)))
+        return EPX_ERR_ARG;
+    if ((st = arm_checks(g)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_combine_backward(g, *layout, dout, y, y_rows, topk_weights, hidden,
+                                                 dy, dweights, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm(const epx_expert_rows *rows, const void *x, const void *w,
+                           int32_t width, int32_t inner, int32_t act, void *preact, void *out,
+                           void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    const bool glu = act == EPX_ACT_SWIGLU;
+    if ((act != EPX_ACT_NONE && !glu) ||
+        !product_sizes_ok(glu ? (int64_t)2 * width : width, width, inner, 8))
+        return EPX_ERR_ARG;
+    if (preact && (!glu || !aligned(preact, 16)))
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || out == x || out == preact)
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(
+        epx::launch_expert_gemm(r, x, w, width, inner, glu, preact, out, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_dgrad(const epx_expert_rows *rows, const void *dy, const void *w,
+                                 int32_t width, int32_t inner, int32_t input_act,
+                                 const void *preact, void *dx, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    const bool glu = input_act == EPX_ACT_SWIGLU;
+    if ((input_act != EPX_ACT_NONE && !glu) || !product_sizes_ok(width, width, inner, 8) ||
+        (!glu && preact))
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(dy, 16) || !ready(w, 16) || !ready(dx, 16) || (glu && !ready(preact, 16)) ||
+        dx == dy || dx == preact)
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_dgrad(r, dy, w, width, inner, preact, dx,
+                                             (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_wgrad(const epx_expert_rows *rows, const void *dy, const void *x,
+                                 int32_t width, int32_t inner, int32_t dw_dtype,
+                                 int32_t accumulate, void *dw, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    if ((dw_dtype != EPX_BF16 && dw_dtype != EPX_F32) || (accumulate != 0 && accumulate != 1) ||
+        (accumulate && dw_dtype != EPX_F32) || !product_sizes_ok(width, width, inner, 8))
+        return EPX_ERR_ARG;
+    if (!ready(dw, 16) || (r.num_rows > 0 && (!ready(dy, 16) || !ready(x, 16))))
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_wgrad(r, dy, x, width, inner, dw_dtype == EPX_F32,
+                                             accumulate != 0, dw, (hipStream_t)stream));
+}
+
+epx_status epx_mxfp4_quantize(const void *x, int64_t num_rows, int32_t inner, uint8_t *codes,
+                              uint8_t *scales, void *stream)
+{
+    HookScope hook_scope;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || inner < 32 || inner % 32 != 0)
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(codes, 16) || !scales)
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_mxfp4_quantize(x, num_rows, inner, codes, scales, (hipStream_t)stream));
+}
+
+epx_status epx_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t num_rows,
+                                int32_t inner, void *out, void *stream)
+{
+    HookScope hook_scope;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || inner < 32 || inner % 32 != 0)
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(out, 16) || !ready(codes, 16) || !scales)
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_mxfp4_dequantize(codes, scales, num_rows, inner, out, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint8_t *x,
+                                 const float *x_scales, const uint8_t *w, const uint8_t *w_scales,
+                                 int32_t width, int32_t inner, int32_t act, int32_t out_dtype,
+                                 void *out, float *out_scales, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    const bool glu = act == EPX_ACT_SWIGLU, fp8 = out_dtype == EPX_FP8_E4M3;
+    if ((act != EPX_ACT_NONE && !glu) || (out_dtype != EPX_BF16 && !fp8) ||
+        !product_sizes_ok(glu ? (int64_t)2 * width : width, width, inner, epx::kFp8Block) ||
+        (fp8 && width % epx::kFp8Block != 0))
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || !ready(x_scales, 4) ||
+        !ready(w_scales, 4) || (fp8 && !ready(out_scales, 4)) || out == x)
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_gemm_mxfp4(r, x, x_scales, w, w_scales, width, inner, glu,
+                                                  fp8, out, out_scales, (hipStream_t)stream));
 }
 
 }  // extern "C"

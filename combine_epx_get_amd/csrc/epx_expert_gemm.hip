@@ -1,0 +1,431 @@
+// epx_expert_gemm.hip -- the experts' products on ragged row ranges, and
+// their gradients, on the matrix cores of gfx950 (bf16 in, float32 sums).
+//
+//   forward  out[r, n]  = sum_k x[r, k] w[e][n, k]     (P = w, Q = x)
+//   dgrad    dx[r, k]   = sum_n dy[r, n] w[e][n, k]    (P = w, Q = dy)
+//   wgrad    dw[e][n,k] = sum_r dy[r, n] x[r, k]       (P = x, Q = dy)
+//
+// Tiles of TP x TQ results; the operands come to LDS in steps of BK along
+// the sum, by direct copies (no registers), in a ring of S buffers, so that
+// S - 1 steps are under way while one is multiplied.
+//
+// An operand whose sum index is contiguous in memory is kept as rows of BK
+// (a fragment is one 16-byte read); one whose sum index is the row in memory
+// as rows of the tile's columns (a fragment is two transposing reads of 8
+// bytes). The 16-byte chunks of a row are permuted by an exclusive or with
+// bits of the row index, in the copies' source addresses, so that the reads
+// of a fragment touch every LDS bank equally.
+//
+// Reads past an operand's last row, column or sum index return zeros (the
+// buffer descriptors' range check), so ragged tiles need no other code; a
+// tile writes the rows and columns that exist.
+#include "epx_gemm.h"
+
+namespace epx {
+namespace {
+
+enum Op { kForward, kForwardGlu, kDgrad, kDgradGlu, kWgrad };
+
+struct Args {
+    ExpertRows r;
+    const char *p, *q;      // operands
+    int32_t np, nq;         // P's extent (columns of a P row in memory for the gradients); Q's for wgrad
+    int32_t sum;            // length of the sum (forward, dgrad)
+    int32_t pt, qt;         // tiles along P; along Q (wgrad)
+    const uint16_t *preact_in;
+    uint16_t *preact_out;
+    void *out;
+    int32_t f32, accumulate;
+};
+
+// Which 16-byte chunk of a row a chunk is kept at: exclusive or with these.
+// Rows of BK: the rows of a fragment differ in their low two bits and in bit
+// `high`. Rows of columns: see read_cols.
+template <int HIGH> __device__ __forceinline__ int row_key(int r) { return (r & 3) | (((r >> HIGH) & 1) << 2); }
+__device__ __forceinline__ int col_key(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
+
+__host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
+
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
+    static constexpr bool kGlu = OP == kForwardGlu;
+    static constexpr bool kPCols = OP >= kDgrad;     // P's sum index is the row in memory
+    static constexpr bool kQCols = OP == kWgrad;
+    static constexpr int kWaves = WP * WQ, kThreads = kWaves * kWave;
+    static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
+    // P fragments whose results are merged: a lane then has 4 * GI
+    // consecutive columns
+    static constexpr int kHalf = kGlu ? NI / 2 : NI;
+    static constexpr int GI = kPCols ? 1 : kHalf % 4 == 0 ? 4 : kHalf % 2 == 0 ? 2 : 1;
+    static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
+    static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
+    static constexpr int kLds = S * (kPBytes + kQBytes);
+    static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
+    static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
+
+    // Row of the tile that lane row m (0..15) of P fragment i reads.
+    static __device__ __forceinline__ int p_row(int wp, int i, int m)
+    {
+        if constexpr (kGlu) {
+            const int h = i / kHalf, ii = i % kHalf;
+            return h * (TP / 2) + wp * (TP / 2 / WP) + ii / GI * 16 * GI + 4 * GI * (m >> 2) + ii % GI * 4 + (m & 3);
+        } else {
+            return wp * (TP / WP) + i / GI * 16 * GI + 4 * GI * (m >> 2) + i % GI * 4 + (m & 3);
+        }
+    }
+
+    // Source offsets of a wave's copies of one operand. `extent` rows are
+    // loaded from row0 on (COLS: columns from col0 on); ld is in elements.
+    template <bool COLS, int T, int N, int KEY, bool SPLIT>
+    static __device__ __forceinline__ void copy_offsets(int wave, int row0, int ld, int up, uint32_t (&off)[N])
+    {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const int inst = wave * N + c;
+            if constexpr (COLS) {
+                constexpr int lanes = T / 8;   // lanes per row of the tile
+                const int k = inst * (64 / lanes) + lane_id() / lanes;
+                const int chunk = (lane_id() % lanes) ^ col_key(k);
+                off[c] = (uint32_t)(k * ld + chunk * 8) * 2u;
+            } else {
+                constexpr int lanes = BK / 8;
+                const int r = inst * (64 / lanes) + lane_id() / lanes;
+                const int chunk = (lane_id() % lanes) ^ row_key<KEY>(r);
+                const int src = SPLIT && r >= T / 2 ? up + row0 + r - T / 2 : row0 + r;
+                off[c] = ((uint32_t)src * (uint32_t)ld + chunk * 8) * 2u;
+            }
+        }
+    }
+
+    // One fragment (16 rows or columns by 32 of the sum) of an operand kept
+    // as rows of columns: two transposing reads. Lane (g, 4 j + s) of a read
+    // names 4 columns of sum row g * 8 + j (+ 4); it gets column 4 j + s of
+    // the four rows.
+    template <int T>
+    static __device__ __forceinline__ bf16x8 read_cols(uint32_t buf, int col, int s)
+    {
+        const int l = lane_id(), g = l >> 4, j = (l >> 2) & 3;
+        const int k = s * 32 + g * 8 + j;
+        const int chunk = (col / 8 + ((l & 3) >> 1)) ^ col_key(k);
+        const uint32_t at = buf + k * (T * 2) + chunk * 16 + (l & 1) * 8;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 4 * T * 2));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+
+    template <int KEY>
+    static __device__ __forceinline__ bf16x8 read_rows(uint32_t buf, int row, int s)
+    {
+        const int chunk = (s * 4 + (lane_id() >> 4)) ^ row_key<KEY>(row);
+        return lds_read<bf16x8>(buf + row * (BK * 2) + chunk * 16);
+    }
+
+    static __device__ __forceinline__ void run(const Args &a, char *smem)
+    {
+        const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
+        const int m = lane_id() & 15, g = lane_id() >> 4;
+        constexpr int PK = 2 + log2i(GI), QK = 2;   // row_key bits
+
+        Tile t;
+        int sum = a.sum;
+        if constexpr (OP == kWgrad) {
+            // every expert has pt * qt tiles; an XCD gets neighbours
+            const int tiles = a.pt * a.qt, per = (tiles + kXcds - 1) / kXcds;
+            const int b = blockIdx.x, slots = per * kXcds;
+            t.expert = b / slots;
+            const int local = b - t.expert * slots;
+            const int id = local % kXcds * per + local / kXcds;
+            if (id >= tiles)
+                return;
+            t.p = id % a.pt;
+            t.q = id / a.pt;
+            t.row0 = 0;
+            sum = uniform(rows_of(a.r, t.expert, t.row0));
+            t.row0 = uniform(t.row0);
+            t.rows = TQ;
+        } else {
+            if (!find_tile<TQ>(a.r, a.pt, blockIdx.x, t))
+                return;
+        }
+        const int steps = (sum + BK - 1) / BK;
+        constexpr int PC = kGlu ? TP / 2 : TP;   // output columns of a tile
+        const int col0 = t.p * PC;
+
+        // operand bases and, for operands whose sum index is the memory row, their last byte
+        const char *pb, *qb;
+        uint32_t p_bytes = 0, q_bytes = 0;
+        if constexpr (OP == kWgrad) {
+            pb = a.p + ((int64_t)t.row0 * a.np + col0) * 2;
+            qb = a.q + ((int64_t)t.row0 * a.nq + t.q * TQ) * 2;
+        } else if constexpr (kPCols) {
+            pb = a.p + ((int64_t)t.expert * sum * a.np + col0) * 2;
+            qb = a.q + (int64_t)t.row0 * sum * 2;
+            q_bytes = (uint32_t)min(t.rows, TQ) * (uint32_t)sum * 2u;
+        } else {
+            const int rows = kGlu ? 2 * a.np : a.np;
+            pb = a.p + (int64_t)t.expert * rows * sum * 2;
+            p_bytes = (uint32_t)rows * (uint32_t)sum * 2u;
+            qb = a.q + (int64_t)t.row0 * sum * 2;
+            q_bytes = (uint32_t)min(t.rows, TQ) * (uint32_t)sum * 2u;
+        }
+        pb = uniform_ptr(pb);
+        qb = uniform_ptr(qb);
+        uint32_t p_off[kPCopies], q_off[kQCopies];
+        copy_offsets<kPCols, TP, kPCopies, PK, kGlu>(wave, kPCols ? 0 : col0, kPCols ? a.np : sum, a.np, p_off);
+        copy_offsets<kQCols, TQ, kQCopies, QK, false>(wave, 0, kQCols ? a.nq : sum, 0, q_off);
+        const uint32_t lds = lds_offset(smem);
+
+        auto issue = [&](int step, int buf) {
+            const int k0 = step * BK;
+            const bool live = step < steps;
+            const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
+            i32x4 rp, rq;
+            if constexpr (kPCols)
+                rp = buffer_of(pb + (int64_t)k0 * a.np * 2,
+                               live ? (uint32_t)min(BK, sum - k0) * (uint32_t)a.np * 2u - (uint32_t)col0 * 2u : 0u);
+            else
+                rp = buffer_of(pb + (int64_t)k0 * 2, live ? p_bytes - (uint32_t)k0 * 2u : 0u);
+            if constexpr (kQCols)
+                rq = buffer_of(qb + (int64_t)k0 * a.nq * 2,
+                               live ? (uint32_t)min(BK, sum - k0) * (uint32_t)a.nq * 2u - (uint32_t)t.q * TQ * 2u : 0u);
+            else
+                rq = buffer_of(qb + (int64_t)k0 * 2, live ? q_bytes - (uint32_t)k0 * 2u : 0u);
+            // a last step that ends inside BK: chunks past the sum's end
+            // would be the next row's first
+            const bool tail = live && k0 + BK > sum;
+#pragma unroll
+            for (int c = 0; c < kPCopies; ++c) {
+                const int inst = wave * kPCopies + c;
+                uint32_t o = p_off[c];
+                if (!kPCols && tail) {
+                    const int r = inst * (512 / BK) + lane_id() / (BK / 8);
+                    if (k0 + ((lane_id() % (BK / 8)) ^ row_key<PK>(r)) * 8 >= sum)
+                        o = kOutside;
+                }
+                copy16_to_lds(at + inst * 1024, rp, o);
+            }
+#pragma unroll
+            for (int c = 0; c < kQCopies; ++c) {
+                const int inst = wave * kQCopies + c;
+                uint32_t o = q_off[c];
+                if (!kQCols && tail) {
+                    const int r = inst * (512 / BK) + lane_id() / (BK / 8);
+                    if (k0 + ((lane_id() % (BK / 8)) ^ row_key<QK>(r)) * 8 >= sum)
+                        o = kOutside;
+                }
+                copy16_to_lds(at + kPBytes + inst * 1024, rq, o);
+            }
+        };
+
+        f32x4 acc[NI][NJ];
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s)
+            issue(s, s);
+        int buf = 0;
+        for (int step = 0; step < steps; ++step) {
+            wait_copies<(S - 2) * (kPCopies + kQCopies)>();
+            int into = buf + S - 1;
+            into = into >= S ? into - S : into;
+            issue(step + S - 1, into);
+            const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
+#pragma unroll
+            for (int s = 0; s < BK / 32; ++s) {
+                bf16x8 pf[NI], qf[NJ];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    if constexpr (kPCols)
+                        pf[i] = read_cols<TP>(at, wp * (TP / WP) + i * 16, s);
+                    else
+                        pf[i] = read_rows<PK>(at, p_row(wp, i, m), s);
+                }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if constexpr (kQCols)
+                        qf[j] = read_cols<TQ>(at + kPBytes, wq * (TQ / WQ) + j * 16, s);
+                    else
+                        qf[j] = read_rows<QK>(at + kPBytes, wq * (TQ / WQ) + j * 16 + m, s);
+                }
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+            }
+            buf = buf + 1 == S ? 0 : buf + 1;
+        }
+        drain_copies();
+
+        // results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
+        // columns 4 g .. 4 g + 3 of fragment i, merged over GI fragments
+        constexpr int NG = kHalf / GI;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int r = wq * (TQ / WQ) + j * 16 + m;
+            if constexpr (OP == kWgrad) {
+                const int n = t.q * TQ + r;
+                if (n >= a.nq)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int c = col0 + wp * (TP / WP) + i * 16 + 4 * g;
+                    if (c >= a.np)
+                        continue;
+                    const int64_t o = ((int64_t)t.expert * a.nq + n) * a.np + c;
+                    if (a.f32) {
+                        f32x4 *d = (f32x4 *)((float *)a.out + o);
+                        *d = a.accumulate ? *d + acc[i][j] : acc[i][j];
+                    } else {
+                        *(u32x2 *)((uint16_t *)a.out + o) =
+                            u32x2{pack2(acc[i][j].x, acc[i][j].y), pack2(acc[i][j].z, acc[i][j].w)};
+                    }
+                }
+            } else {
+                if (r >= t.rows)
+                    continue;
+                const int64_t row = t.row0 + r;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    Cols<4 * GI> u, v;
+#pragma unroll
+                    for (int i = 0; i < GI; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            u.v[4 * i + q] = acc[n * GI + i][j][q];
+                            if constexpr (kGlu)
+                                v.v[4 * i + q] = acc[kHalf + n * GI + i][j][q];
+                        }
+                    const int c = col0 + wp * (PC / WP) + n * 16 * GI + 4 * GI * g;
+                    if constexpr (OP == kForward) {
+                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
+                    } else if constexpr (OP == kForwardGlu) {
+                        if (a.preact_out) {
+                            store_bf16(a.preact_out + row * 2 * a.np, c, a.np, u);
+                            store_bf16(a.preact_out + row * 2 * a.np + a.np, c, a.np, v);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4 * GI; ++q)
+                            u.v[q] = swiglu(u.v[q], v.v[q]);
+                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
+                    } else if constexpr (OP == kDgrad) {
+                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
+                    } else {
+                        if (c >= a.np)
+                            continue;
+                        const uint16_t *pre = a.preact_in + row * 2 * a.np + c;
+                        const u32x2 gv = *(const u32x2 *)pre, uv = *(const u32x2 *)(pre + a.np);
+                        const float gate[4] = {bf16_lo(gv.x), bf16_hi(gv.x), bf16_lo(gv.y), bf16_hi(gv.y)};
+                        const float up[4] = {bf16_lo(uv.x), bf16_hi(uv.x), bf16_lo(uv.y), bf16_hi(uv.y)};
+                        Cols<4> dg, du;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float s = sigmoid32(gate[q]);
+                            dg.v[q] = u.v[q] * up[q] * (s * (1.0f + gate[q] * (1.0f - s)));
+                            du.v[q] = u.v[q] * (gate[q] * s);
+                        }
+                        uint16_t *dx = (uint16_t *)a.out + row * 2 * a.np;
+                        store_bf16(dx, c, a.np, dg);
+                        store_bf16(dx + a.np, c, a.np, du);
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
+__global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
+{
+    using K = Kernel<OP, TP, TQ, BK, S, WP, WQ>;
+    __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
+    K::run(a, smem);
+}
+
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
+hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
+{
+    constexpr int PC = OP == kForwardGlu ? TP / 2 : TP;
+    a.pt = (a.np + PC - 1) / PC;
+    int64_t blocks;
+    if (OP == kWgrad) {
+        a.qt = (a.nq + TQ - 1) / TQ;
+        blocks = rows_or_n * tile_blocks((int64_t)a.pt * a.qt);
+    } else {
+        blocks = tile_blocks(most_row_tiles(rows_or_n, a.r.n, TQ) * a.pt);
+    }
+    if (blocks == 0)
+        return hipSuccess;
+    if (blocks * WP * WQ * kWave > (int64_t)0xFFFFFFFF)
+        return hipErrorInvalidConfiguration;
+    launch(gemm_kernel<OP, TP, TQ, BK, S, WP, WQ>, dim3((unsigned)blocks), dim3(WP * WQ * kWave), 0,
+           stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w, int32_t width,
+                              int32_t inner, bool swiglu, void *preact, void *out,
+                              hipStream_t stream)
+{
+    Args a = {};
+    a.r = r;
+    a.p = (const char *)w;
+    a.q = (const char *)x;
+    a.np = width;
+    a.sum = inner;
+    a.preact_out = (uint16_t *)preact;
+    a.out = out;
+    const int64_t avg = r.num_rows / r.n;
+    if (avg > 96)
+        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream)
+                      : start<kForward, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream);
+    if (avg > 16)
+        return swiglu ? start<kForwardGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
+                      : start<kForward, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
+    return swiglu ? start<kForwardGlu, 128, 32, 64, 4, 4, 1>(a, r.num_rows, stream)
+                  : start<kForward, 128, 32, 64, 4, 4, 1>(a, r.num_rows, stream);
+}
+
+hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *w, int32_t width,
+                               int32_t inner, const void *preact, void *dx, hipStream_t stream)
+{
+    Args a = {};
+    a.r = r;
+    a.p = (const char *)w;
+    a.q = (const char *)dy;
+    a.np = inner;
+    a.sum = width;
+    a.preact_in = (const uint16_t *)preact;
+    a.out = dx;
+    const int64_t avg = r.num_rows / r.n;
+    if (avg > 96)
+        return preact ? start<kDgradGlu, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream)
+                      : start<kDgrad, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream);
+    return preact ? start<kDgradGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
+                  : start<kDgrad, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
+}
+
+hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *x, int32_t width,
+                               int32_t inner, bool f32, bool accumulate, void *dw,
+                               hipStream_t stream)
+{
+    Args a = {};
+    a.r = r;
+    a.p = (const char *)x;
+    a.q = (const char *)dy;
+    a.np = inner;
+    a.nq = width;
+    a.out = dw;
+    a.f32 = f32;
+    a.accumulate = accumulate;
+    if ((int64_t)width * inner >= 2048 * 2048)
+        return start<kWgrad, 256, 256, 64, 2, 2, 2>(a, r.n, stream);
+    return start<kWgrad, 128, 128, 64, 3, 2, 2>(a, r.n, stream);
+}
+
+}  // namespace epx

@@ -1,0 +1,353 @@
+// epx_expert_mxfp4.hip -- the experts' products of fp8 rows (E4M3, a float32
+// scale per 128 channels) with 4-bit weights (MXFP4) on the matrix cores of
+// gfx950.
+//
+//   out[r, n] = sum over blocks b of 128 channels of
+//               x_scale[r, b] * sum_{k in b} x[r, k] w[e][n, k]
+//
+// The scaled matrix instruction 16x16x128 takes 4-bit values with their
+// power-of-two scale per 32 along the sum in one operand (P = w) and E4M3
+// codes in the other (Q = x): one instruction spans one of x's scale blocks,
+// so its result is multiplied by the row's float32 scale and added to the
+// float32 sum (the instruction's own scale of Q is 1).
+//
+// Operand places in the instruction: P, row lane % 16, 32 values 32 * (lane /
+// 16) on; Q, the 16 codes from 16 * (lane / 16) on and the 16 from 64 + 16 *
+// (lane / 16) on. Tiles, copies, ring of buffers and chunk permutation as in
+// the bf16 products; the scales come to LDS beside the codes.
+#include "epx_gemm.h"
+
+namespace epx {
+namespace {
+
+struct Args {
+    ExpertRows r;
+    const char *w, *ws, *x, *xs;
+    int32_t np;    // output columns
+    int32_t sum;   // channels summed over (inner)
+    int32_t pt;    // tiles along the columns
+    void *out;
+    float *out_scales;
+};
+
+__host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
+
+// SUBS blocks of 128 channels a step.
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ> struct Kernel {
+    static constexpr int kWaves = WP * WQ;
+    static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
+    static constexpr int kHalf = GLU ? NI / 2 : NI;
+    static constexpr int GI = kHalf % 4 == 0 ? 4 : kHalf % 2 == 0 ? 2 : 1;
+    static constexpr int PC = GLU ? TP / 2 : TP;
+    static constexpr int kPRow = 64 * SUBS, kQRow = 128 * SUBS;   // bytes of a row in LDS
+    static constexpr int kPBytes = TP * kPRow, kQBytes = TQ * kQRow;
+    static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
+    // scale words: one of 4 bytes per row and block, 64 rows a copy; rounded
+    // up so that every wave makes the same number of copies
+    static constexpr int kPScale = TP / 64, kQScale = (TQ + 63) / 64;
+    static constexpr int kScales = SUBS * (kPScale + kQScale);
+    static constexpr int kSCopies = (kScales + kWaves - 1) / kWaves;
+    static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
+    static constexpr int kLds = S * kBuf;
+    static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
+    static_assert(!GLU || NI % 2 == 0, "gate and up fragments pair up in a wave");
+    static_assert(!FP8OUT || PC % 128 == 0, "a tile holds whole scale blocks");
+    static_assert(TP % 64 == 0 && SUBS <= 2, "");
+
+    static __device__ __forceinline__ int p_row(int wp, int i, int m)
+    {
+        if constexpr (GLU) {
+            const int h = i / kHalf, ii = i % kHalf;
+            return h * (TP / 2) + wp * (TP / 2 / WP) + ii / GI * 16 * GI + 4 * GI * (m >> 2) + ii % GI * 4 + (m & 3);
+        } else {
+            return wp * (TP / WP) + i / GI * 16 * GI + 4 * GI * (m >> 2) + i % GI * 4 + (m & 3);
+        }
+    }
+    // Rows of 64 bytes (4 chunks): neighbours already differ in their half of
+    // the banks; rows of 128 bytes and more as in the bf16 products.
+    static __device__ __forceinline__ int p_key(int r)
+    {
+        constexpr int H = 2 + log2i(GI);
+        if constexpr (SUBS == 1)
+            return ((r >> 1) & 1) | (((r >> H) & 1) << 1);
+        else
+            return (r & 3) | (((r >> H) & 1) << 2);
+    }
+    static __device__ __forceinline__ int q_key(int r) { return (r & 3) | (((r >> 2) & 1) << 2); }
+
+    static __device__ __forceinline__ void run(const Args &a, char *smem)
+    {
+        const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
+        const int lane = lane_id(), m = lane & 15, g = lane >> 4;
+        Tile t;
+        if (!find_tile<TQ>(a.r, a.pt, blockIdx.x, t))
+            return;
+        const int blocks = a.sum / 128, steps = (blocks + SUBS - 1) / SUBS;
+        const int col0 = t.p * PC;
+        const int mat_rows = GLU ? 2 * a.np : a.np, qrows = min(t.rows, TQ);
+        const uint32_t sld = (uint32_t)a.sum / 32u;   // bytes of scales in a row, of either operand
+
+        const char *pb = uniform_ptr(a.w + (int64_t)t.expert * mat_rows * (a.sum / 2));
+        const char *psb = uniform_ptr(a.ws + (int64_t)t.expert * mat_rows * sld);
+        const char *qb = uniform_ptr(a.x + (int64_t)t.row0 * a.sum);
+        const char *qsb = uniform_ptr(a.xs + (int64_t)t.row0 * sld);
+        const uint32_t p_bytes = (uint32_t)mat_rows * ((uint32_t)a.sum / 2u), ps_bytes = (uint32_t)mat_rows * sld;
+        const uint32_t q_bytes = (uint32_t)qrows * (uint32_t)a.sum, qs_bytes = (uint32_t)qrows * sld;
+
+        auto weight_row = [&](int r) { return GLU && r >= TP / 2 ? a.np + col0 + r - TP / 2 : col0 + r; };
+        uint32_t p_off[kPCopies], q_off[kQCopies], s_off[kSCopies];
+#pragma unroll
+        for (int c = 0; c < kPCopies; ++c) {
+            constexpr int lanes = kPRow / 16;
+            const int r = (wave * kPCopies + c) * (64 / lanes) + lane / lanes;
+            p_off[c] = (uint32_t)weight_row(r) * ((uint32_t)a.sum / 2u) + (((lane % lanes) ^ p_key(r)) * 16);
+        }
+#pragma unroll
+        for (int c = 0; c < kQCopies; ++c) {
+            constexpr int lanes = kQRow / 16;
+            const int r = (wave * kQCopies + c) * (64 / lanes) + lane / lanes;
+            q_off[c] = (uint32_t)r * (uint32_t)a.sum + (((lane % lanes) ^ q_key(r)) * 16);
+        }
+        // scale copies: [sub][P rows in 64s, Q rows in 64s]
+#pragma unroll
+        for (int c = 0; c < kSCopies; ++c) {
+            const int inst = wave * kSCopies + c, sub = inst / (kPScale + kQScale), i = inst % (kPScale + kQScale);
+            const bool is_p = i < kPScale;
+            const int r = (is_p ? i : i - kPScale) * 64 + lane;
+            const bool in = inst < kScales && (is_p ? r < TP : r < TQ);
+            s_off[c] = in ? (uint32_t)(is_p ? weight_row(r) : r) * sld + (uint32_t)sub * 4u : kOutside;
+        }
+        const uint32_t lds = lds_offset(smem);
+
+        auto issue = [&](int step, int buf) {
+            const bool live = step < steps;
+            const int b0 = step * SUBS;   // first block of 128
+            const uint32_t at = lds + (uint32_t)buf * kBuf;
+            const i32x4 rp = buffer_of(pb + (int64_t)b0 * 64, live ? p_bytes - (uint32_t)b0 * 64u : 0u);
+            const i32x4 rq = buffer_of(qb + (int64_t)b0 * 128, live ? q_bytes - (uint32_t)b0 * 128u : 0u);
+            const i32x4 rps = buffer_of(psb + (int64_t)b0 * 4, live ? ps_bytes - (uint32_t)b0 * 4u : 0u);
+            const i32x4 rqs = buffer_of(qsb + (int64_t)b0 * 4, live ? qs_bytes - (uint32_t)b0 * 4u : 0u);
+            // a last step of fewer blocks: what lies past the sum's end would
+            // be the next row's first
+            const bool tail = SUBS > 1 && live && b0 + SUBS > blocks;
+#pragma unroll
+            for (int c = 0; c < kPCopies; ++c) {
+                const int inst = wave * kPCopies + c;
+                uint32_t o = p_off[c];
+                if (tail) {
+                    constexpr int lanes = kPRow / 16;
+                    const int r = inst * (64 / lanes) + lane / lanes;
+                    if ((((lane % lanes) ^ p_key(r)) >> 2) + b0 >= blocks)
+                        o = kOutside;
+                }
+                copy16_to_lds(at + inst * 1024, rp, o);
+            }
+#pragma unroll
+            for (int c = 0; c < kQCopies; ++c) {
+                const int inst = wave * kQCopies + c;
+                uint32_t o = q_off[c];
+                if (tail) {
+                    constexpr int lanes = kQRow / 16;
+                    const int r = inst * (64 / lanes) + lane / lanes;
+                    if ((((lane % lanes) ^ q_key(r)) >> 3) + b0 >= blocks)
+                        o = kOutside;
+                }
+                copy16_to_lds(at + kPBytes + inst * 1024, rq, o);
+            }
+#pragma unroll
+            for (int c = 0; c < kSCopies; ++c) {
+                const int inst = wave * kSCopies + c, sub = inst / (kPScale + kQScale);
+                const bool is_p = inst % (kPScale + kQScale) < kPScale;
+                copy4_to_lds(at + kPBytes + kQBytes + inst * 256, is_p ? rps : rqs,
+                             tail && b0 + sub >= blocks ? kOutside : s_off[c]);
+            }
+        };
+
+        f32x4 acc[NI][NJ];
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s)
+            issue(s, s);
+        int buf = 0;
+        for (int step = 0; step < steps; ++step) {
+            wait_copies<(S - 2) * (kPCopies + kQCopies + kSCopies)>();
+            int into = buf + S - 1;
+            into = into >= S ? into - S : into;
+            issue(step + S - 1, into);
+            const uint32_t at = lds + (uint32_t)buf * kBuf;
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s) {
+                const uint32_t ps = at + kPBytes + kQBytes + s * (kPScale + kQScale) * 256, qs = ps + kPScale * 256;
+                i32x8 pf[NI];
+                int sp[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int r = p_row(wp, i, m);
+                    const i32x4 v = lds_read<i32x4>(at + r * kPRow + (((s * 4 + g) ^ p_key(r)) * 16));
+                    pf[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+                    sp[i] = lds_read<uint8_t>(ps + r * 4 + g);
+                }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const int r = wq * (TQ / WQ) + j * 16 + m;
+                    const uint32_t row = at + kPBytes + r * kQRow;
+                    const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
+                    const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
+                    const i32x8 qf = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const float sq = lds_read<float>(qs + r * 4);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf, zero, 4, 0, 0, sp[i],
+                                                                                         0, 127);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            acc[i][j][q] = __builtin_fmaf(d[q], sq, acc[i][j][q]);
+                    }
+                }
+            }
+            buf = buf + 1 == S ? 0 : buf + 1;
+        }
+        drain_copies();
+
+        constexpr int NG = kHalf / GI;
+        if constexpr (FP8OUT) {
+            // activation in place, then the largest magnitude of every row in
+            // each block of 128 columns: over a wave's lanes, then over the
+            // waves that share the block
+            constexpr int kBlocks = PC / 128, kPerBlock = WP / kBlocks;
+            static_assert(kBlocks <= WP, "");
+            float *s_max = (float *)smem;   // [WP][TQ]
+            __syncthreads();                // every wave is done with the operands
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                float mx = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (GLU)
+                            acc[i][j][q] = swiglu(acc[i][j][q], acc[kHalf + i][j][q]);
+                        mx = fmaxf(mx, fabsf(acc[i][j][q]));
+                    }
+                mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
+                mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+                if (g == 0)
+                    s_max[wp * TQ + wq * (TQ / WQ) + j * 16 + m] = mx;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int r = wq * (TQ / WQ) + j * 16 + m;
+                if (r >= t.rows)
+                    continue;
+                const int64_t row = t.row0 + r;
+                const int blk = wp / kPerBlock;
+                float mx = 0.0f;
+                for (int q = 0; q < kPerBlock; ++q)
+                    mx = fmaxf(mx, s_max[(blk * kPerBlock + q) * TQ + r]);
+                const float sc = mx / 448.0f;
+                if (col0 + blk * 128 >= a.np)
+                    continue;
+                if (g == 0 && wp % kPerBlock == 0)
+                    a.out_scales[row * (a.np / 128) + col0 / 128 + blk] = sc;
+                uint8_t *out = (uint8_t *)a.out + row * a.np;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const int c = col0 + wp * (PC / WP) + n * 16 * GI + 4 * GI * g;
+#pragma unroll
+                    for (int i = 0; i < GI; ++i) {
+                        const f32x4 v = acc[n * GI + i][j];
+                        // a zero block keeps its zeros' signs
+                        const float d = sc == 0.0f ? 1.0f : sc;
+                        *(uint32_t *)(out + c + 4 * i) = e4m3_pair(v.x / d, v.y / d) | (e4m3_pair(v.z / d, v.w / d) << 16);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int r = wq * (TQ / WQ) + j * 16 + m;
+                if (r >= t.rows)
+                    continue;
+                uint16_t *out = (uint16_t *)a.out + (int64_t)(t.row0 + r) * a.np;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    Cols<4 * GI> u;
+#pragma unroll
+                    for (int i = 0; i < GI; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            u.v[4 * i + q] = acc[n * GI + i][j][q];
+                            if constexpr (GLU)
+                                u.v[4 * i + q] = swiglu(u.v[4 * i + q], acc[kHalf + n * GI + i][j][q]);
+                        }
+                    store_bf16(out, col0 + wp * (PC / WP) + n * 16 * GI + 4 * GI * g, a.np, u);
+                }
+            }
+        }
+    }
+};
+
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ>
+__global__ __launch_bounds__(WP *WQ *kWave) void mx_kernel(Args a)
+{
+    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>;
+    __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
+    K::run(a, smem);
+}
+
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ>
+hipError_t start(Args a, hipStream_t stream)
+{
+    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>;
+    a.pt = (a.np + K::PC - 1) / K::PC;
+    const int64_t blocks = tile_blocks(most_row_tiles(a.r.num_rows, a.r.n, TQ) * a.pt);
+    if (blocks == 0)
+        return hipSuccess;
+    if (blocks * WP * WQ * kWave > (int64_t)0xFFFFFFFF)
+        return hipErrorInvalidConfiguration;
+    launch(mx_kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>, dim3((unsigned)blocks), dim3(WP * WQ * kWave), 0,
+           stream, a);
+    return hipGetLastError();
+}
+
+template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stream)
+{
+    const int64_t avg = a.r.num_rows / a.r.n;
+    if (avg > 96)
+        return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 2>(a, stream);
+    constexpr int TP = GLU && FP8OUT ? 256 : 128;
+    if (avg > 16)
+        return start<GLU, FP8OUT, TP, 64, 2, 3, 4, 1>(a, stream);
+    return start<GLU, FP8OUT, TP, 32, 2, 3, 4, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_expert_gemm_mxfp4(const ExpertRows &r, const uint8_t *x, const float *x_scales,
+                                    const uint8_t *w, const uint8_t *w_scales, int32_t width,
+                                    int32_t inner, bool swiglu, bool fp8_out, void *out,
+                                    float *out_scales, hipStream_t stream)
+{
+    Args a = {};
+    a.r = r;
+    a.w = (const char *)w;
+    a.ws = (const char *)w_scales;
+    a.x = (const char *)x;
+    a.xs = (const char *)x_scales;
+    a.np = width;
+    a.sum = inner;
+    a.out = out;
+    a.out_scales = out_scales;
+    if (fp8_out)
+        return swiglu ? pick<true, true>(a, stream) : pick<false, true>(a, stream);
+    return swiglu ? pick<true, false>(a, stream) : pick<false, false>(a, stream);
+}
+
+}  // namespace epx

@@ -1,0 +1,199 @@
+// epx_gemm.h -- pieces shared by the grouped matrix products (internal).
+//
+// A product's two operands are P, whose index runs along the contiguous
+// direction of the output, and Q, whose index is the output row. P is the
+// first operand of the matrix instruction, so that the four results of a
+// lane are four consecutive elements of an output row.
+#pragma once
+
+#include "epx_device.h"
+
+namespace epx {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kXcds = 8;
+// A byte offset behind the end of every buffer (buffers hold at most 2^31
+// bytes): loads there return zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+
+template <int V> using Int = std::integral_constant<int, V>;
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ const char *uniform_ptr(const void *p)
+{
+    const uint64_t a = (uint64_t)p;
+    const uint32_t lo = (uint32_t)uniform((int)a), hi = (uint32_t)uniform((int)(a >> 32));
+    return (const char *)(((uint64_t)hi << 32) | lo);
+}
+
+// Buffer descriptor of `bytes` bytes from `base`: reads past them give zeros.
+__device__ __forceinline__ i32x4 buffer_of(const char *base, uint32_t bytes)
+{
+    const uint64_t a = (uint64_t)base;
+    i32x4 r;
+    r.x = uniform((int)a);
+    r.y = uniform((int)(a >> 32) & 0xFFFF);
+    r.z = uniform((int)bytes);
+    r.w = 0x00020000;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+}
+
+// 16 bytes a lane from the buffer to LDS at lds + 16 * lane (lds uniform).
+// The copy is asynchronous: wait_copies() orders it.
+__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4 buf, uint32_t offset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 0\n\t"
+                 "buffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(offset), "s"(buf)
+                 : "memory");
+}
+
+// 4 bytes a lane to LDS at lds + 4 * lane.
+__device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4 buf, uint32_t offset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 0\n\t"
+                 "buffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(offset), "s"(buf)
+                 : "memory");
+}
+
+// Waits until at most PENDING of this wave's copies are under way and its
+// own LDS reads are done, then for the workgroup's other waves: afterwards
+// every wave's waited-for copies are visible, and what was read before may
+// be overwritten.
+template <int PENDING> __device__ __forceinline__ void wait_copies()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
+}
+
+// Every copy of this wave is done (before its LDS is given back).
+__device__ __forceinline__ void drain_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <typename T> __device__ __forceinline__ T lds_read(uint32_t at)
+{
+    return *(const __attribute__((address_space(3))) T *)(uintptr_t)at;
+}
+
+// ---------------------------------------------------------------- tiles
+// Rows of expert e, 0 for a range outside the buffers.
+__device__ __forceinline__ int rows_of(const ExpertRows &r, int e, int &off)
+{
+    if (e >= r.n)
+        return 0;
+    off = r.offset[e];
+    const int c = r.count[e];
+    if (c <= 0)
+        return 0;
+    if (off < 0 || (int64_t)off + c > r.num_rows) {
+        if (kChecked)
+            atomicAdd(r.viol, 1ull);
+        return 0;
+    }
+    return c;
+}
+
+struct Tile {
+    int expert;
+    int row0, rows;   // first row of the tile and rows from there to the expert's end
+    int p, q;         // tile indexes along P and (within the expert) Q
+};
+
+// Tile of workgroup `b` out of `blocks` for products whose row tiles are
+// ragged: expert e has ceil(rows / TQ) row tiles with pt column tiles each.
+// Consecutive workgroups run on different XCDs, so each XCD gets a contiguous
+// eighth of the tiles that there are; in it, GQ row tiles by GP = 4 column
+// tiles are neighbours, which share what they read through the XCD's L2.
+// Every wave computes the same. False when there is no tile for this
+// workgroup.
+template <int TQ>
+__device__ __forceinline__ bool find_tile(const ExpertRows &r, int pt, int b, Tile &t)
+{
+    constexpr int GQ = 8;
+    const int lane = lane_id();
+    int total = 0;
+    for (int e0 = 0; e0 < r.n; e0 += kWave) {
+        int off;
+        const int c = rows_of(r, e0 + lane, off);
+        total += __builtin_amdgcn_readlane(wave_inclusive_scan((c + TQ - 1) / TQ), kWave - 1);
+    }
+    const int64_t tiles = (int64_t)total * pt;
+    const int64_t per = (tiles + kXcds - 1) / kXcds;
+    const int64_t id = (int64_t)(b % kXcds) * per + b / kXcds;
+    if (b / kXcds >= per || id >= tiles)
+        return false;
+    const int64_t grp = id / ((int64_t)GQ * pt);
+    const int rem = (int)(id - grp * GQ * pt);
+    const int q0 = (int)grp * GQ;
+    const int gq = total - q0 < GQ ? total - q0 : GQ;
+    t.p = rem / gq;
+    const int q = q0 + rem - t.p * gq;
+    int before = 0;
+    for (int e0 = 0; e0 < r.n; e0 += kWave) {
+        int off = 0;
+        const int c = rows_of(r, e0 + lane, off);
+        const int nt = (c + TQ - 1) / TQ;
+        const int incl = wave_inclusive_scan(nt) + before;
+        const uint64_t past = __ballot(incl > q);
+        if (past != 0) {
+            const int win = __builtin_ctzll(past);
+            t.expert = e0 + win;
+            t.q = q - (__builtin_amdgcn_readlane(incl, win) - __builtin_amdgcn_readlane(nt, win));
+            t.row0 = __builtin_amdgcn_readlane(off, win) + t.q * TQ;
+            t.rows = __builtin_amdgcn_readlane(c, win) - t.q * TQ;
+            return true;
+        }
+        before = __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+    return false;
+}
+
+// Row tiles of TQ rows that n experts with rows rows in all can have.
+inline int64_t most_row_tiles(int64_t rows, int n, int tq)
+{
+    return rows / tq + (rows < n ? rows : n);
+}
+
+// Workgroups for `tiles` tiles at most (a multiple of the XCDs).
+inline int64_t tile_blocks(int64_t tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
+
+// ---------------------------------------------------------------- activation
+__device__ __forceinline__ float sigmoid32(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+__device__ __forceinline__ float swiglu(float gate, float up) { return gate * sigmoid32(gate) * up; }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) { return f32_to_bf16(a) | (f32_to_bf16(b) << 16); }
+
+// Widths of the vectors that hold a lane's N consecutive results.
+template <int N> struct Cols { float v[N]; };
+
+// Columns [c, c + N) of a bf16 row that has `width` columns (a multiple of 8).
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int width, const Cols<N> &o)
+{
+    if constexpr (N == 4) {
+        if (c < width)
+            *(u32x2 *)(row + c) = u32x2{pack2(o.v[0], o.v[1]), pack2(o.v[2], o.v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            if (c + i < width)
+                *(u32x4 *)(row + c + i) = u32x4{pack2(o.v[i], o.v[i + 1]), pack2(o.v[i + 2], o.v[i + 3]),
+                                                pack2(o.v[i + 4], o.v[i + 5]), pack2(o.v[i + 6], o.v[i + 7])};
+    }
+}
+
+}  // namespace epx

@@ -29,6 +29,10 @@ MODE_HOST_RELAY = 1
 BF16 = 0
 FP8_E4M3 = 1
 F32 = 2
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+ACT_NONE = 0
+ACT_SWIGLU = 1
 
 STATUS = {0: "EPX_OK", 1: "EPX_ERR_ARG", 2: "EPX_ERR_INDEX", 3: "EPX_ERR_CAPACITY", 4: "EPX_ERR_DEVICE",
           5: "EPX_ERR_SCRATCH"}
@@ -48,6 +52,11 @@ class epx_problem(ctypes.Structure):
 
 class epx_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in LAYOUT_FIELDS]
+
+
+class epx_expert_rows(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+                ("row_offset", ctypes.c_void_p), ("row_count", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -76,6 +85,19 @@ _lib.epx_combine_group.argtypes = [ctypes.POINTER(epx_problem), ctypes.POINTER(e
                                    _P, ctypes.c_int64, _P, ctypes.c_int32, _P, _P, _P]
 _lib.epx_plan_swaps.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int32,
                                 _P, _P, _P, _P, _P, _P]
+_I32 = ctypes.c_int32
+_lib.epx_route.argtypes = [ctypes.POINTER(epx_problem), _P, _I32, _I32, _P, _I32, ctypes.c_float, _P, _P, _P]
+_lib.epx_route_backward.argtypes = [ctypes.POINTER(epx_problem), _P, _I32, _I32, _I32, ctypes.c_float, _P, _P,
+                                    _P, _P]
+_lib.epx_combine_backward.argtypes = [ctypes.POINTER(epx_problem), ctypes.POINTER(epx_layout), _P, _P,
+                                      ctypes.c_int64, _P, _I32, _P, _P, _P]
+_lib.epx_expert_gemm.argtypes = [ctypes.POINTER(epx_expert_rows), _P, _P, _I32, _I32, _I32, _P, _P, _P]
+_lib.epx_expert_gemm_dgrad.argtypes = [ctypes.POINTER(epx_expert_rows), _P, _P, _I32, _I32, _I32, _P, _P, _P]
+_lib.epx_expert_gemm_wgrad.argtypes = [ctypes.POINTER(epx_expert_rows), _P, _P, _I32, _I32, _I32, _I32, _P, _P]
+_lib.epx_mxfp4_quantize.argtypes = [_P, ctypes.c_int64, _I32, _P, _P, _P]
+_lib.epx_mxfp4_dequantize.argtypes = [_P, _P, ctypes.c_int64, _I32, _P, _P]
+_lib.epx_expert_gemm_mxfp4.argtypes = [ctypes.POINTER(epx_expert_rows), _P, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                       _P, _P, _P]
 _lib.epx_time_next_call.argtypes = [_P, _P]
 _lib.epx_checked_violations.argtypes = [ctypes.POINTER(ctypes.c_int64), _P]
 _lib.epx_status_string.argtypes = [ctypes.c_int]
@@ -84,7 +106,9 @@ for _f in ("epx_layout_sizes", "epx_get_layout", "epx_dispatch", "epx_combine", 
            "epx_f32_to_e4m3", "epx_relay_fanout", "epx_combine_relay_partials",
            "epx_combine_relay_finish", "epx_plan_swaps", "epx_dispatch_group", "epx_combine_group",
            "epx_layout_dispatch", "epx_time_next_call", "epx_layout_dispatch_noalloc",
-           "epx_checked_violations"):
+           "epx_checked_violations", "epx_route", "epx_route_backward", "epx_combine_backward",
+           "epx_expert_gemm", "epx_expert_gemm_dgrad", "epx_expert_gemm_wgrad", "epx_mxfp4_quantize",
+           "epx_mxfp4_dequantize", "epx_expert_gemm_mxfp4"):
     getattr(_lib, _f).restype = ctypes.c_int
 _lib.epx_abi_version.restype = ctypes.c_int32
 NARRAYS = len(LAYOUT_FIELDS)
@@ -391,6 +415,210 @@ def epx_plan_swaps(num_experts: int, num_ranks: int, num_hosts: int, expert_coun
                                out["host_bad"].data_ptr(), _stream(stream)),
            "epx_plan_swaps")
     return out
+
+
+_LOGITS = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _route_args(problem, logits, topk_idx, name, other):
+    shape = (problem.num_tokens, problem.topk)
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
+        raise ValueError("logits: bfloat16 or float32")
+    _need(logits, logits.dtype, "logits", 2)
+    if tuple(logits.shape) != (problem.num_tokens, problem.num_experts):
+        raise ValueError("logits: need [T, E]")
+    _need(topk_idx, torch.int32, "topk_idx", 2)
+    _need(other, torch.float32, name, 2)
+    if tuple(topk_idx.shape) != shape or tuple(other.shape) != shape:
+        raise ValueError(f"topk_idx, {name}: need [T, k]")
+
+
+def epx_route(problem: epx_problem, logits: torch.Tensor, score: int, topk_idx: torch.Tensor,
+              topk_weights: torch.Tensor, bias: Optional[torch.Tensor] = None, renormalize: bool = True,
+              scale: float = 1.0, stream=None) -> None:
+    """Router: the k experts of every token and their weights, from logits [T, E]."""
+    _route_args(problem, logits, topk_idx, "topk_weights", topk_weights)
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.numel() != problem.num_experts:
+            raise ValueError("bias: need [E]")
+    _check(_lib.epx_route(ctypes.byref(problem), logits.data_ptr(), _LOGITS[logits.dtype], score,
+                          bias.data_ptr() if bias is not None else None, int(bool(renormalize)), scale,
+                          topk_idx.data_ptr(), topk_weights.data_ptr(), _stream(stream)), "epx_route")
+
+
+def epx_route_backward(problem: epx_problem, logits: torch.Tensor, score: int, topk_idx: torch.Tensor,
+                       dweights: torch.Tensor, dlogits: torch.Tensor, renormalize: bool = True,
+                       scale: float = 1.0, stream=None) -> None:
+    """Gradient of epx_route's weights: dlogits [T, E] from dweights [T, k]."""
+    _route_args(problem, logits, topk_idx, "dweights", dweights)
+    _need(dlogits, logits.dtype, "dlogits", 2)
+    if dlogits.shape != logits.shape:
+        raise ValueError("dlogits: need [T, E]")
+    _check(_lib.epx_route_backward(ctypes.byref(problem), logits.data_ptr(), _LOGITS[logits.dtype], score,
+                                   int(bool(renormalize)), scale, topk_idx.data_ptr(), dweights.data_ptr(),
+                                   dlogits.data_ptr(), _stream(stream)), "epx_route_backward")
+
+
+def epx_combine_backward(problem: epx_problem, layout: Layout, dout: torch.Tensor, y: Optional[torch.Tensor],
+                         topk_weights: torch.Tensor, dy: torch.Tensor,
+                         dweights: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of epx_combine: dy (rows of y) and, if given, dweights [T, k]
+    (without it y is not read and may be None)."""
+    _need(dout, torch.bfloat16, "dout", 2)
+    _need(topk_weights, torch.float32, "topk_weights", 2)
+    _need(dy, torch.bfloat16, "dy", 2)
+    shape = (problem.num_tokens, problem.topk)
+    if tuple(topk_weights.shape) != shape:
+        raise ValueError("topk_weights: need [T, k]")
+    if dout.shape[0] != problem.num_tokens or dout.shape[1] != dy.shape[1]:
+        raise ValueError("dout: need [T, hidden]")
+    if dweights is not None:
+        _need(dweights, torch.float32, "dweights", 2)
+        _need(y, torch.bfloat16, "y", 2)
+        if tuple(dweights.shape) != shape:
+            raise ValueError("dweights: need [T, k]")
+        if y.shape != dy.shape:
+            raise ValueError("y: need the shape of dy")
+    _check(_lib.epx_combine_backward(ctypes.byref(problem), ctypes.byref(layout.struct), dout.data_ptr(),
+                                     y.data_ptr() if dweights is not None else None, dy.shape[0],
+                                     topk_weights.data_ptr(), dout.shape[1], dy.data_ptr(),
+                                     dweights.data_ptr() if dweights is not None else None, _stream(stream)),
+           "epx_combine_backward")
+
+
+class ExpertRows:
+    """Row ranges of the experts on this GPU (device tensors) and the matching C struct."""
+
+    def __init__(self, row_offset: torch.Tensor, row_count: torch.Tensor, num_rows: int):
+        _need(row_offset, torch.int32, "row_offset", 1)
+        _need(row_count, torch.int32, "row_count", 1)
+        if row_offset.numel() < row_count.numel():
+            raise ValueError("row_offset: need an entry for every expert of row_count")
+        if not 0 <= num_rows < 1 << 31:
+            raise ValueError("num_rows: need 0 <= num_rows < 2^31")
+        self.row_offset, self.row_count = row_offset, row_count
+        self.num_experts, self.num_rows = row_count.numel(), int(num_rows)
+        self.struct = epx_expert_rows(self.num_experts, self.num_rows, row_offset.data_ptr(), row_count.data_ptr())
+
+
+def expert_rows(row_offset: torch.Tensor, row_count: torch.Tensor, num_rows: int) -> ExpertRows:
+    """Rows [row_offset[e], row_offset[e] + row_count[e]) for each expert e, in
+    buffers of num_rows rows. A layout's arrays serve as they are:
+    expert_rows(L["expert_offset"], L["expert_count"], T * k)."""
+    return ExpertRows(row_offset, row_count, num_rows)
+
+
+def _shape(t, dtype, name, *shape):
+    _need(t, dtype, name, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: need shape {list(shape)}, got {list(t.shape)}")
+
+
+def epx_expert_gemm(rows: ExpertRows, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, act: int = ACT_NONE,
+                    preact: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[r] = act(x[r] @ w[e].T) for the rows r of every expert e. With
+    ACT_SWIGLU w is [n, 2 * width, inner] (gate rows, then up rows) and preact,
+    if given, receives the product before the activation."""
+    _need(out, torch.bfloat16, "out", 2)
+    _need(x, torch.bfloat16, "x", 2)
+    width, inner, R = out.shape[1], x.shape[1], rows.num_rows
+    wide = 2 * width if act == ACT_SWIGLU else width
+    _shape(x, torch.bfloat16, "x", R, inner)
+    _shape(out, torch.bfloat16, "out", R, width)
+    _shape(w, torch.bfloat16, "w", rows.num_experts, wide, inner)
+    if preact is not None:
+        _shape(preact, torch.bfloat16, "preact", R, wide)
+    _check(_lib.epx_expert_gemm(ctypes.byref(rows.struct), x.data_ptr(), w.data_ptr(), width, inner, act,
+                                preact.data_ptr() if preact is not None else None, out.data_ptr(),
+                                _stream(stream)), "epx_expert_gemm")
+
+
+def epx_expert_gemm_dgrad(rows: ExpertRows, dy: torch.Tensor, w: torch.Tensor, dx: torch.Tensor,
+                          input_act: int = ACT_NONE, preact: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx[r] = dy[r] @ w[e]; with input_act=ACT_SWIGLU (the product's input was
+    the gated activation of preact) dx is the gradient of preact."""
+    _need(w, torch.bfloat16, "w", 3)
+    width, inner, R = w.shape[1], w.shape[2], rows.num_rows
+    wide = 2 * inner if input_act == ACT_SWIGLU else inner
+    _shape(w, torch.bfloat16, "w", rows.num_experts, width, inner)
+    _shape(dy, torch.bfloat16, "dy", R, width)
+    _shape(dx, torch.bfloat16, "dx", R, wide)
+    if preact is not None:
+        _shape(preact, torch.bfloat16, "preact", R, wide)
+    _check(_lib.epx_expert_gemm_dgrad(ctypes.byref(rows.struct), dy.data_ptr(), w.data_ptr(), width, inner,
+                                      input_act, preact.data_ptr() if preact is not None else None,
+                                      dx.data_ptr(), _stream(stream)), "epx_expert_gemm_dgrad")
+
+
+def epx_expert_gemm_wgrad(rows: ExpertRows, dy: torch.Tensor, x: torch.Tensor, dw: torch.Tensor,
+                          accumulate: bool = False, stream=None) -> None:
+    """dw[e] = dy[r].T @ x[r] summed over the rows of every expert e; bfloat16
+    or float32, the latter also added to what dw holds."""
+    if not isinstance(dw, torch.Tensor) or dw.dtype not in _LOGITS:
+        raise ValueError("dw: bfloat16 or float32")
+    _need(dw, dw.dtype, "dw", 3)
+    width, inner, R = dw.shape[1], dw.shape[2], rows.num_rows
+    _shape(dw, dw.dtype, "dw", rows.num_experts, width, inner)
+    _shape(dy, torch.bfloat16, "dy", R, width)
+    _shape(x, torch.bfloat16, "x", R, inner)
+    _check(_lib.epx_expert_gemm_wgrad(ctypes.byref(rows.struct), dy.data_ptr(), x.data_ptr(), width, inner,
+                                      _LOGITS[dw.dtype], int(bool(accumulate)), dw.data_ptr(),
+                                      _stream(stream)), "epx_expert_gemm_wgrad")
+
+
+def _mxfp4_args(values, codes, scales, name):
+    """Rows are the product of all dimensions but the last."""
+    _need(values, torch.bfloat16, name)
+    _need(codes, torch.uint8, "codes")
+    _need(scales, torch.uint8, "scales")
+    if values.dim() < 2:
+        raise ValueError(f"{name}: need at least 2 dimensions")
+    inner = values.shape[-1]
+    lead = tuple(values.shape[:-1])
+    if inner % 32 or tuple(codes.shape) != lead + (inner // 2,) or tuple(scales.shape) != lead + (inner // 32,):
+        raise ValueError("codes, scales: need [..., inner/2] and [..., inner/32], inner a multiple of 32")
+    return values.numel() // inner if inner else 0, inner
+
+
+def epx_mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """bf16 rows [..., inner] to 4-bit codes [..., inner/2] and scale bytes [..., inner/32]."""
+    num_rows, inner = _mxfp4_args(x, codes, scales, "x")
+    _check(_lib.epx_mxfp4_quantize(x.data_ptr(), num_rows, inner, codes.data_ptr(), scales.data_ptr(),
+                                   _stream(stream)), "epx_mxfp4_quantize")
+
+
+def epx_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """The bf16 values that 4-bit codes and scale bytes stand for."""
+    num_rows, inner = _mxfp4_args(out, codes, scales, "out")
+    _check(_lib.epx_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), num_rows, inner, out.data_ptr(),
+                                     _stream(stream)), "epx_mxfp4_dequantize")
+
+
+def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                          w_scales: torch.Tensor, out: torch.Tensor, act: int = ACT_NONE,
+                          out_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """epx_expert_gemm for fp8 rows (codes and a float32 scale per 128 channels,
+    as epx_dispatch writes them) and 4-bit weights. out is bfloat16, or uint8
+    codes with out_scales [rows, width/128]."""
+    fp8 = isinstance(out, torch.Tensor) and out.dtype == torch.uint8
+    _need(out, torch.uint8 if fp8 else torch.bfloat16, "out", 2)
+    _need(x, torch.uint8, "x", 2)
+    width, inner, R, n = out.shape[1], x.shape[1], rows.num_rows, rows.num_experts
+    wide = 2 * width if act == ACT_SWIGLU else width
+    _shape(x, torch.uint8, "x", R, inner)
+    _shape(x_scales, torch.float32, "x_scales", R, inner // 128)
+    _shape(w, torch.uint8, "w", n, wide, inner // 2)
+    _shape(w_scales, torch.uint8, "w_scales", n, wide, inner // 32)
+    _shape(out, out.dtype, "out", R, width)
+    if fp8:
+        _shape(out_scales, torch.float32, "out_scales", R, width // 128)
+    elif out_scales is not None:
+        raise ValueError("out_scales: only with uint8 rows out")
+    _check(_lib.epx_expert_gemm_mxfp4(ctypes.byref(rows.struct), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(),
+                                      w_scales.data_ptr(), width, inner, act, FP8_E4M3 if fp8 else BF16,
+                                      out.data_ptr(), out_scales.data_ptr() if fp8 else None,
+                                      _stream(stream)), "epx_expert_gemm_mxfp4")
 
 
 def relay_capacity(problem: epx_problem) -> int:

@@ -17,6 +17,14 @@
  *   epx_relay_fanout, epx_combine_relay_partials, epx_combine_relay_finish
  *                    -- the relay's receive side and its two-level combine
  *   epx_plan_swaps   -- per-step expert swaps between GPUs of one host
+ *   epx_route        -- router scores -> topk_idx and topk_weights
+ *   epx_expert_gemm  -- the experts' products on the per-expert rows, with a
+ *                       gated activation in their epilogue; their gradients
+ *                       are epx_expert_gemm_dgrad and epx_expert_gemm_wgrad
+ *   epx_expert_gemm_mxfp4 -- fp8 rows times 4-bit weights, which
+ *                       epx_mxfp4_quantize makes
+ *   epx_combine_backward, epx_route_backward -- gradients of the two
+ *                       (dispatch's gradient is epx_combine with weights 1)
  *
  * Conventions for every call:
  *  - Every array argument is a DEVICE pointer the caller allocated; the
@@ -353,6 +361,154 @@ EPX_API epx_status epx_plan_swaps(int32_t num_experts, int32_t num_ranks, int32_
                                   int32_t tau, int32_t *slot_expert_out,
                                   int32_t *rank_load_before, int32_t *rank_load_after,
                                   int32_t *swaps, int32_t *host_bad, void *stream);
+
+/* ---- Router. Scores, choice and weights of the k experts of every token,
+ * as epx_get_layout and epx_combine take them. The problem gives T, E and k
+ * (k <= 64, E <= 2048; its ranks, hosts, mode and groups play no part).
+ *  logits       [T, E], EPX_BF16 or EPX_F32, 16-byte aligned
+ *  score        EPX_SCORE_SOFTMAX: p = softmax over the E logits of a token;
+ *               EPX_SCORE_SIGMOID: p = 1 / (1 + exp(-logit))
+ *  bias         float32 [E] or NULL: added to a sigmoid score for the choice
+ *               only (p + bias, in 64 bits); with softmax it must be NULL
+ *  renormalize  0: w = scale * p;  1: w = scale * p / (sum of the chosen p)
+ *  topk_idx     int32 [T, k], the k largest keys in descending order (the
+ *               key is the logit, or p + bias); equal keys by ascending id
+ *  topk_weights float32 [T, k]
+ * A logit of -infinity or NaN masks its expert: score 0, chosen (in order of
+ * id) only when a token has fewer than k others. A token with nothing left
+ * gets weights 0. Masked experts rank below every other one, whatever their
+ * bias. A softmax over logits of +infinity shares the weight among them.
+ * Errors: EPX_ERR_ARG. */
+typedef enum { EPX_SCORE_SOFTMAX = 0, EPX_SCORE_SIGMOID = 1 } epx_score;
+
+EPX_API epx_status epx_route(const epx_problem *p, const void *logits, int32_t logits_dtype,
+                             int32_t score, const float *bias, int32_t renormalize, float scale,
+                             int32_t *topk_idx, float *topk_weights, void *stream);
+
+/* Gradient of epx_route's weights: dlogits [T, E] (logits_dtype, every
+ * element written) from dweights float32 [T, k] and the ids that epx_route
+ * chose. The choice itself has no gradient (nor has the bias); masked experts
+ * get 0. An id outside [0, E) contributes nothing; an id that is given twice
+ * counts twice. Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_route_backward(const epx_problem *p, const void *logits,
+                                      int32_t logits_dtype, int32_t score, int32_t renormalize,
+                                      float scale, const int32_t *topk_idx, const float *dweights,
+                                      void *dlogits, void *stream);
+
+/* Gradient of epx_combine: with dout bf16 [T, hidden] and combine's y and
+ * weights,
+ *   dy[slot[t, j], :]  = bf16( topk_weights[t, j] * dout[t, :] )
+ *   dweights[t, j]     = sum over channels of dout[t, :] * y[slot[t, j], :]
+ * (float32, in a fixed order). dy has y_rows rows; rows that no slot names
+ * are left untouched. dweights may be NULL: then y is not read and may be
+ * NULL too. hidden is a multiple of 8; expert groups share one call. Errors
+ * as epx_combine; after a layout that saw bad ids nothing is written. */
+EPX_API epx_status epx_combine_backward(const epx_problem *p, const epx_layout *layout,
+                                        const void *dout, const void *y, int64_t y_rows,
+                                        const float *topk_weights, int32_t hidden, void *dy,
+                                        float *dweights, void *stream);
+
+/* ---- The experts' products. Expert e of the num_experts on this GPU owns
+ * the rows [row_offset[e], row_offset[e] + row_count[e]) of every row buffer
+ * (device arrays; a layout's expert_offset and expert_count, or a part of
+ * them, serve as they are). An expert may have no rows; ranges may leave
+ * gaps and come in any order but must not overlap. Rows outside every range
+ * are neither read nor written. A range that is not inside [0, num_rows)
+ * counts as empty (the bounds-checked build counts it, see
+ * epx_checked_violations).
+ * Limits: 1 <= num_experts <= 2048, 0 <= num_rows < 2^31. */
+typedef struct {
+    int32_t num_experts;
+    int32_t num_rows;            /* rows of the buffers that the ranges address */
+    const int32_t *row_offset;   /* [num_experts] */
+    const int32_t *row_count;    /* [num_experts] */
+} epx_expert_rows;
+
+/* EPX_ACT_SWIGLU: the product has 2 * width columns, gates then ups, and the
+ * output is silu(gate) * up = gate / (1 + exp(-gate)) * up. */
+typedef enum { EPX_ACT_NONE = 0, EPX_ACT_SWIGLU = 1 } epx_act;
+
+/* out[r, :] = act( x[r, :] * w[e]^T ) for every row r of expert e.
+ *  x       bf16 [num_rows, inner]
+ *  w       bf16 [num_experts, width, inner]; with EPX_ACT_SWIGLU
+ *          [num_experts, 2 * width, inner], the gate rows before the up rows
+ *  out     bf16 [num_rows, width]
+ *  preact  NULL, or with EPX_ACT_SWIGLU bf16 [num_rows, 2 * width]: the
+ *          product before the activation, which epx_expert_gemm_dgrad takes
+ * Products are summed in float32 and rounded once, to bf16 (nearest even);
+ * the activation is computed from the float32 sums. width and inner are
+ * multiples of 8 of at most 2^20, rows of one expert's matrix times inner at
+ * most 2^30; every pointer is 16-byte aligned. The buffers must not overlap.
+ * Errors: EPX_ERR_ARG; EPX_ERR_DEVICE also for more tiles than one launch
+ * can have (2^32 threads). */
+EPX_API epx_status epx_expert_gemm(const epx_expert_rows *rows, const void *x, const void *w,
+                                   int32_t width, int32_t inner, int32_t act, void *preact,
+                                   void *out, void *stream);
+
+/* Gradient of a product's input: d[r, :] = dy[r, :] * w[e], with dy bf16
+ * [num_rows, width] and w bf16 [num_experts, width, inner].
+ *  input_act EPX_ACT_NONE:   dx = d, bf16 [num_rows, inner]
+ *  input_act EPX_ACT_SWIGLU: the product's input was silu(gate) * up of
+ *            preact bf16 [num_rows, 2 * inner]; dx, bf16 [num_rows,
+ *            2 * inner], is the gradient of preact:
+ *            d gate = d * up * s * (1 + gate * (1 - s)), d up = d * gate * s
+ *            with s = 1 / (1 + exp(-gate))
+ * Sums, the activation's gradient and rounding as in epx_expert_gemm.
+ * Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_dgrad(const epx_expert_rows *rows, const void *dy,
+                                         const void *w, int32_t width, int32_t inner,
+                                         int32_t input_act, const void *preact, void *dx,
+                                         void *stream);
+
+/* Gradient of the weights: dw[e] = sum over the expert's rows r of
+ * dy[r, :]^T * x[r, :], for dy bf16 [num_rows, width] and x bf16 [num_rows,
+ * inner]; dw is EPX_BF16 or EPX_F32 [num_experts, width, inner]. With
+ * accumulate (EPX_F32 only) the sum is added to dw, else dw is overwritten
+ * (with 0 for an expert without rows). Sums in float32, in a fixed order.
+ * Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_wgrad(const epx_expert_rows *rows, const void *dy,
+                                         const void *x, int32_t width, int32_t inner,
+                                         int32_t dw_dtype, int32_t accumulate, void *dw,
+                                         void *stream);
+
+/* ---- 4-bit weights (OCP Microscaling Formats: MXFP4). 32 consecutive
+ * values of a row share one scale byte b (2^(b-127)); a value is an E2M1 code
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times the scale, two codes
+ * to a byte, the even value in the low half.
+ * Quantisation: scale = 2^(floor(log2(max |v|)) - 2), at least 2^-127; code =
+ * v / scale rounded to nearest even, saturated at 6 (the specification's
+ * conversion). A block of zeros has scale byte 0; a block that holds an
+ * infinity or NaN has scale byte 255, which reads as NaN.
+ *  x       bf16 [num_rows, inner], inner a multiple of 32, num_rows < 2^31
+ *  codes   uint8 [num_rows, inner / 2]
+ *  scales  uint8 [num_rows, inner / 32]
+ * x, out and codes are 16-byte aligned. Dequantisation is exact.
+ * Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_mxfp4_quantize(const void *x, int64_t num_rows, int32_t inner,
+                                      uint8_t *codes, uint8_t *scales, void *stream);
+EPX_API epx_status epx_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales,
+                                        int64_t num_rows, int32_t inner, void *out, void *stream);
+
+/* epx_expert_gemm for fp8 rows, as epx_dispatch writes them, and 4-bit
+ * weights:
+ *  x         uint8 [num_rows, inner] E4M3 codes, x_scales float32 [num_rows,
+ *            inner / 128]
+ *  w         uint8 [num_experts, width or 2 * width, inner / 2], w_scales
+ *            uint8 [num_experts, width or 2 * width, inner / 32], as
+ *            epx_mxfp4_quantize writes them
+ *  out_dtype EPX_BF16: out bf16 [num_rows, width]; EPX_FP8_E4M3: out uint8
+ *            [num_rows, width] and out_scales float32 [num_rows, width / 128],
+ *            quantised from the float32 results by the rule of epx_dispatch,
+ *            so that another such product can follow
+ * Sums in float32: every 128 channels of codes, then times the row's scale.
+ * inner is a multiple of 128, width of 8 (of 128 for fp8 rows out), rows of
+ * one expert's matrix times inner at most 2^30; x, w, out are 16-byte
+ * aligned, the scales to 4 bytes. The buffers must not overlap. Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint8_t *x,
+                                         const float *x_scales, const uint8_t *w,
+                                         const uint8_t *w_scales, int32_t width, int32_t inner,
+                                         int32_t act, int32_t out_dtype, void *out,
+                                         float *out_scales, void *stream);
 
 /* Synchronises `stream`, then reads totals[3]: EPX_OK, or EPX_ERR_INDEX when
  * the last layout on this layout's arrays saw out-of-range expert ids (their
