@@ -59,6 +59,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
     static constexpr int kLds = S * (kPBytes + kQBytes);
+    static constexpr bool kDeep = S == 2;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
 
@@ -174,11 +175,11 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         copy_offsets<kQCols, TQ, kQCopies, QK, false>(wave, 0, kQCols ? a.nq : sum, 0, q_off);
         const uint32_t lds = lds_offset(smem);
 
-        auto issue = [&](int step, int buf) {
+        // descriptors of the operands' parts in a step (empty past the last)
+        i32x4 rp, rq;
+        auto aim = [&](int step) {
             const int k0 = step * BK;
             const bool live = step < steps;
-            const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
-            i32x4 rp, rq;
             if constexpr (kPCols)
                 rp = buffer_of(pb + (int64_t)k0 * a.np * 2,
                                live ? (uint32_t)min(BK, sum - k0) * (uint32_t)a.np * 2u - (uint32_t)col0 * 2u : 0u);
@@ -190,30 +191,45 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
             else
                 rq = buffer_of(qb + (int64_t)k0 * 2, live ? q_bytes - (uint32_t)k0 * 2u : 0u);
             // a last step that ends inside BK: chunks past the sum's end
-            // would be the next row's first
-            const bool tail = live && k0 + BK > sum;
+            // would be the next row's first (no live step follows it)
+            if (!(kPCols && kQCols) && live && k0 + BK > sum) {
 #pragma unroll
-            for (int c = 0; c < kPCopies; ++c) {
-                const int inst = wave * kPCopies + c;
-                uint32_t o = p_off[c];
-                if (!kPCols && tail) {
-                    const int r = inst * (512 / BK) + lane_id() / (BK / 8);
+                for (int c = 0; c < kPCopies && !kPCols; ++c) {
+                    const int r = (wave * kPCopies + c) * (512 / BK) + lane_id() / (BK / 8);
                     if (k0 + ((lane_id() % (BK / 8)) ^ row_key<PK>(r)) * 8 >= sum)
-                        o = kOutside;
+                        p_off[c] = kOutside;
                 }
-                copy16_to_lds(at + inst * 1024, rp, o);
-            }
 #pragma unroll
-            for (int c = 0; c < kQCopies; ++c) {
-                const int inst = wave * kQCopies + c;
-                uint32_t o = q_off[c];
-                if (!kQCols && tail) {
-                    const int r = inst * (512 / BK) + lane_id() / (BK / 8);
+                for (int c = 0; c < kQCopies && !kQCols; ++c) {
+                    const int r = (wave * kQCopies + c) * (512 / BK) + lane_id() / (BK / 8);
                     if (k0 + ((lane_id() % (BK / 8)) ^ row_key<QK>(r)) * 8 >= sum)
-                        o = kOutside;
+                        q_off[c] = kOutside;
                 }
-                copy16_to_lds(at + kPBytes + inst * 1024, rq, o);
             }
+        };
+        auto copy = [&](int c, uint32_t at) {
+            if (c < kPCopies)
+                copy16_to_lds(at + (wave * kPCopies + c) * 1024, rp, p_off[c]);
+            else
+                copy16_to_lds(at + kPBytes + (wave * kQCopies + c - kPCopies) * 1024, rq, q_off[c - kPCopies]);
+        };
+        auto issue = [&](int step, int buf) {
+            aim(step);
+#pragma unroll
+            for (int c = 0; c < kPCopies + kQCopies; ++c)
+                copy(c, lds + (uint32_t)buf * (kPBytes + kQBytes));
+        };
+        auto read_p = [&](uint32_t at, int i, int s) {
+            if constexpr (kPCols)
+                return read_cols<TP>(at, wp * (TP / WP) + i * 16, s);
+            else
+                return read_rows<PK>(at, p_row(wp, i, m), s);
+        };
+        auto read_q = [&](uint32_t at, int j, int s) {
+            if constexpr (kQCols)
+                return read_cols<TQ>(at + kPBytes, wq * (TQ / WQ) + j * 16, s);
+            else
+                return read_rows<QK>(at + kPBytes, wq * (TQ / WQ) + j * 16 + m, s);
         };
 
         f32x4 acc[NI][NJ];
@@ -223,40 +239,89 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
             for (int j = 0; j < NJ; ++j)
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+        if constexpr (kDeep) {
+            // Two buffers, and two sets of fragments in registers: while one
+            // half of a step (32 of the sum) is multiplied, the next half's
+            // fragments are read. The buffer of a step is free for the copies
+            // of the step after next as soon as its second half is read, and
+            // one meeting of the waves per step, between the halves, orders
+            // both that and the arrival of the next step.
+            static_assert(S == 2 && BK == 64 && NI == 8 && NJ == 8, "");
+            constexpr uint32_t kBuf = kPBytes + kQBytes;
+            constexpr int kCopies = kPCopies + kQCopies;
+            bf16x8 pf[2][8], qf[2][8];
+            auto read = [&](int set, uint32_t at, int c) {
+                if (c < 8)
+                    qf[set][c] = read_q(at, c, set);
+                else
+                    pf[set][c - 8] = read_p(at, c - 8, set);
+            };
+            issue(0, 0);
+            issue(1, 1);
+            wait_copies<kCopies>();
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s)
-            issue(s, s);
-        int buf = 0;
-        for (int step = 0; step < steps; ++step) {
-            wait_copies<(S - 2) * (kPCopies + kQCopies)>();
-            int into = buf + S - 1;
-            into = into >= S ? into - S : into;
-            issue(step + S - 1, into);
-            const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
+            for (int c = 0; c < 16; ++c)
+                read(0, lds, c);
+            uint32_t at = lds, next = lds + kBuf;
+            for (int step = 0; step < steps; ++step) {
 #pragma unroll
-            for (int s = 0; s < BK / 32; ++s) {
-                bf16x8 pf[NI], qf[NJ];
+                for (int i = 0; i < 8; ++i) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    if constexpr (kPCols)
-                        pf[i] = read_cols<TP>(at, wp * (TP / WP) + i * 16, s);
-                    else
-                        pf[i] = read_rows<PK>(at, p_row(wp, i, m), s);
+                    for (int c = i * 3; c < i * 3 + 3 && c < 16; ++c)
+                        read(1, at, c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mfma_in_place(acc[i][j], pf[0][i], qf[0][j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                wait_copies<0>();
+                aim(step + 2);
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    if constexpr (kQCols)
-                        qf[j] = read_cols<TQ>(at + kPBytes, wq * (TQ / WQ) + j * 16, s);
-                    else
-                        qf[j] = read_rows<QK>(at + kPBytes, wq * (TQ / WQ) + j * 16 + m, s);
+                for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                    for (int c = i * 3; c < i * 3 + 3 && c < 16; ++c)
+                        read(0, next, c);
+#pragma unroll
+                    for (int c = i * 3; c < i * 3 + 3 && c < kCopies; ++c)
+                        copy(c, at);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                const uint32_t swap = at;
+                at = next;
+                next = swap;
+            }
+            mfma_settle();
+        } else {
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
+            for (int s = 0; s < S - 1; ++s)
+                issue(s, s);
+            int buf = 0;
+            for (int step = 0; step < steps; ++step) {
+                wait_copies<(S - 2) * (kPCopies + kQCopies)>();
+                int into = buf + S - 1;
+                into = into >= S ? into - S : into;
+                issue(step + S - 1, into);
+                const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
+#pragma unroll
+                for (int s = 0; s < BK / 32; ++s) {
+                    bf16x8 pf[NI], qf[NJ];
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        pf[i] = read_p(at, i, s);
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+                        qf[j] = read_q(at, j, s);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+                }
+                buf = buf + 1 == S ? 0 : buf + 1;
             }
-            buf = buf + 1 == S ? 0 : buf + 1;
         }
         drain_copies();
 

@@ -89,6 +89,20 @@ template <typename T> __device__ __forceinline__ T lds_read(uint32_t at)
     return *(const __attribute__((address_space(3))) T *)(uintptr_t)at;
 }
 
+// c += a b with the sum held in the accumulation registers throughout: left
+// to itself the compiler moves sums that fill all 256 of them between the two
+// register files inside the loop. It does not know this for a matrix
+// instruction, so nothing but another one (of another sum, or at least four
+// later) may follow until mfma_settle().
+__device__ __forceinline__ void mfma_in_place(f32x4 &c, bf16x8 a, bf16x8 b)
+{
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// After the last of them, before the sums are read: the longest wait that a
+// result of a 16x16 instruction can need.
+__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
 // ---------------------------------------------------------------- tiles
 // Rows of expert e, 0 for a range outside the buffers.
 __device__ __forceinline__ int rows_of(const ExpertRows &r, int e, int &off)
