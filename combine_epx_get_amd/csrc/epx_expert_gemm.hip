@@ -120,33 +120,13 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         return lds_read<bf16x8>(buf + row * (BK * 2) + chunk * 16);
     }
 
-    static __device__ __forceinline__ void run(const Args &a, char *smem)
+    static __device__ __forceinline__ void run(const Args &a, const Tile &t, char *smem)
     {
         const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
         const int m = lane_id() & 15, g = lane_id() >> 4;
         constexpr int PK = 2 + log2i(GI), QK = 2;   // row_key bits
 
-        Tile t;
-        int sum = a.sum;
-        if constexpr (OP == kWgrad) {
-            // every expert has pt * qt tiles; an XCD gets neighbours
-            const int tiles = a.pt * a.qt, per = (tiles + kXcds - 1) / kXcds;
-            const int b = blockIdx.x, slots = per * kXcds;
-            t.expert = b / slots;
-            const int local = b - t.expert * slots;
-            const int id = local % kXcds * per + local / kXcds;
-            if (id >= tiles)
-                return;
-            t.p = id % a.pt;
-            t.q = id / a.pt;
-            t.row0 = 0;
-            sum = uniform(rows_of(a.r, t.expert, t.row0));
-            t.row0 = uniform(t.row0);
-            t.rows = TQ;
-        } else {
-            if (!find_tile<TQ>(a.r, a.pt, blockIdx.x, t))
-                return;
-        }
+        const int sum = OP == kWgrad ? t.sum : a.sum;
         const int steps = (sum + BK - 1) / BK;
         constexpr int PC = kGlu ? TP / 2 : TP;   // output columns of a tile
         const int col0 = t.p * PC;
@@ -246,46 +226,48 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
             // of the step after next as soon as its second half is read, and
             // one meeting of the waves per step, between the halves, orders
             // both that and the arrival of the next step.
-            static_assert(S == 2 && BK == 64 && NI == 8 && NJ == 8, "");
+            static_assert(S == 2 && BK == 64, "");
             constexpr uint32_t kBuf = kPBytes + kQBytes;
-            constexpr int kCopies = kPCopies + kQCopies;
-            bf16x8 pf[2][8], qf[2][8];
+            constexpr int kCopies = kPCopies + kQCopies, kReads = NI + NJ;
+            // reads and copies before each of the NI rounds of NJ instructions
+            constexpr int kReadsPer = (kReads + NI - 2) / (NI - 1), kCopiesPer = (kCopies + NI - 1) / NI;
+            bf16x8 pf[2][NI], qf[2][NJ];
             auto read = [&](int set, uint32_t at, int c) {
-                if (c < 8)
+                if (c < NJ)
                     qf[set][c] = read_q(at, c, set);
                 else
-                    pf[set][c - 8] = read_p(at, c - 8, set);
+                    pf[set][c - NJ] = read_p(at, c - NJ, set);
             };
             issue(0, 0);
             issue(1, 1);
             wait_copies<kCopies>();
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < kReads; ++c)
                 read(0, lds, c);
             uint32_t at = lds, next = lds + kBuf;
             for (int step = 0; step < steps; ++step) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < NI; ++i) {
 #pragma unroll
-                    for (int c = i * 3; c < i * 3 + 3 && c < 16; ++c)
+                    for (int c = i * kReadsPer; c < (i + 1) * kReadsPer && c < kReads; ++c)
                         read(1, at, c);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < NJ; ++j)
                         mfma_in_place(acc[i][j], pf[0][i], qf[0][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 wait_copies<0>();
                 aim(step + 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < NI; ++i) {
 #pragma unroll
-                    for (int c = i * 3; c < i * 3 + 3 && c < 16; ++c)
+                    for (int c = i * kReadsPer; c < (i + 1) * kReadsPer && c < kReads; ++c)
                         read(0, next, c);
 #pragma unroll
-                    for (int c = i * 3; c < i * 3 + 3 && c < kCopies; ++c)
+                    for (int c = i * kCopiesPer; c < (i + 1) * kCopiesPer && c < kCopies; ++c)
                         copy(c, at);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < NJ; ++j)
                         mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -402,12 +384,43 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     }
 };
 
+// The large tiles' kernels carry the smaller ones for an expert's last rows.
 template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
 __global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
 {
     using K = Kernel<OP, TP, TQ, BK, S, WP, WQ>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
-    K::run(a, smem);
+    Tile t;
+    if constexpr (OP == kWgrad) {
+        // every expert has pt * qt tiles; an XCD gets neighbours
+        const int tiles = a.pt * a.qt, per = (tiles + kXcds - 1) / kXcds;
+        const int b = blockIdx.x, slots = per * kXcds;
+        t.expert = b / slots;
+        const int local = b - t.expert * slots;
+        const int id = local % kXcds * per + local / kXcds;
+        if (id >= tiles)
+            return;
+        t.p = id % a.pt;
+        t.q = id / a.pt;
+        t.row0 = 0;
+        t.sum = uniform(rows_of(a.r, t.expert, t.row0));
+        t.row0 = uniform(t.row0);
+        t.rows = TQ;
+        K::run(a, t, smem);
+    } else {
+        if (!find_tile<TQ, K::kDeep>(a.r, a.pt, blockIdx.x, t))
+            return;
+        if constexpr (K::kDeep) {
+            if (t.rows <= TQ / 4)
+                Kernel<OP, TP, TQ / 4, BK, S, WP, WQ>::run(a, t, smem);
+            else if (t.rows <= TQ / 2)
+                Kernel<OP, TP, TQ / 2, BK, S, WP, WQ>::run(a, t, smem);
+            else
+                K::run(a, t, smem);
+        } else {
+            K::run(a, t, smem);
+        }
+    }
 }
 
 template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
@@ -420,7 +433,7 @@ hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
         a.qt = (a.nq + TQ - 1) / TQ;
         blocks = rows_or_n * tile_blocks((int64_t)a.pt * a.qt);
     } else {
-        blocks = tile_blocks(most_row_tiles(rows_or_n, a.r.n, TQ) * a.pt);
+        blocks = tile_blocks(most_row_tiles(rows_or_n, a.r.n, TQ) * a.pt, Kernel<OP, TP, TQ, BK, S, WP, WQ>::kDeep);
     }
     if (blocks == 0)
         return hipSuccess;
@@ -447,8 +460,8 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
     a.out = out;
     const int64_t avg = r.num_rows / r.n;
     if (avg > 96)
-        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream)
-                      : start<kForward, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream);
+        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
+                      : start<kForward, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
     if (avg > 16)
         return swiglu ? start<kForwardGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
                       : start<kForward, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
@@ -469,8 +482,8 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     a.out = dx;
     const int64_t avg = r.num_rows / r.n;
     if (avg > 96)
-        return preact ? start<kDgradGlu, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream)
-                      : start<kDgrad, 256, 256, 64, 2, 2, 2>(a, r.num_rows, stream);
+        return preact ? start<kDgradGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
+                      : start<kDgrad, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
     return preact ? start<kDgradGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
                   : start<kDgrad, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
 }
@@ -489,7 +502,7 @@ hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *
     a.f32 = f32;
     a.accumulate = accumulate;
     if ((int64_t)width * inner >= 2048 * 2048)
-        return start<kWgrad, 256, 256, 64, 2, 2, 2>(a, r.n, stream);
+        return start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
     return start<kWgrad, 128, 128, 64, 3, 2, 2>(a, r.n, stream);
 }
 

@@ -80,7 +80,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
         const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
         const int lane = lane_id(), m = lane & 15, g = lane >> 4;
         Tile t;
-        if (!find_tile<TQ>(a.r, a.pt, blockIdx.x, t))
+        if (!find_tile<TQ, false>(a.r, a.pt, blockIdx.x, t))
             return;
         const int blocks = a.sum / 128, steps = (blocks + SUBS - 1) / SUBS;
         const int col0 = t.p * PC;

@@ -125,30 +125,56 @@ struct Tile {
     int expert;
     int row0, rows;   // first row of the tile and rows from there to the expert's end
     int p, q;         // tile indexes along P and (within the expert) Q
+    int sum;          // the expert's rows, where they are summed over
 };
 
-// Tile of workgroup `b` out of `blocks` for products whose row tiles are
-// ragged: expert e has ceil(rows / TQ) row tiles with pt column tiles each.
-// Consecutive workgroups run on different XCDs, so each XCD gets a contiguous
-// eighth of the tiles that there are; in it, GQ row tiles by GP = 4 column
-// tiles are neighbours, which share what they read through the XCD's L2.
-// Every wave computes the same. False when there is no tile for this
-// workgroup.
-template <int TQ>
+// Row tiles of an expert with c rows. SPLIT: a last tile of at most TQ / 2
+// rows is small, and small tiles are counted (and run) apart.
+template <int TQ, bool SPLIT> __device__ __forceinline__ int row_tiles(int c, bool small)
+{
+    const int rem = c % TQ;
+    if (!SPLIT)
+        return small ? 0 : c / TQ + (rem > 0);
+    return small ? rem > 0 && rem <= TQ / 2 : c / TQ + (rem > TQ / 2);
+}
+
+// Tile of workgroup `b` for products whose row tiles are ragged: expert e has
+// ceil(rows / TQ) row tiles with pt column tiles each. Consecutive workgroups
+// run on different XCDs, so each XCD gets a contiguous eighth of the tiles
+// that there are; in it, GQ row tiles by GP = 4 column tiles are neighbours,
+// which share what they read through the XCD's L2. Small tiles come after all
+// others: they fill the last round of workgroups, which whole tiles would
+// leave mostly idle (32768 rows on 16 experts: 136 to 144 row tiles of 256,
+// where 128 would do). Every wave computes the same. False when there is no
+// tile for this workgroup.
+template <int TQ, bool SPLIT>
 __device__ __forceinline__ bool find_tile(const ExpertRows &r, int pt, int b, Tile &t)
 {
     constexpr int GQ = 8;
     const int lane = lane_id();
-    int total = 0;
+    int whole = 0, part = 0;
     for (int e0 = 0; e0 < r.n; e0 += kWave) {
         int off;
         const int c = rows_of(r, e0 + lane, off);
-        total += __builtin_amdgcn_readlane(wave_inclusive_scan((c + TQ - 1) / TQ), kWave - 1);
+        whole += __builtin_amdgcn_readlane(wave_inclusive_scan(row_tiles<TQ, SPLIT>(c, false)), kWave - 1);
+        if (SPLIT)
+            part += __popcll(__ballot(row_tiles<TQ, SPLIT>(c, true) > 0));
     }
-    const int64_t tiles = (int64_t)total * pt;
-    const int64_t per = (tiles + kXcds - 1) / kXcds;
-    const int64_t id = (int64_t)(b % kXcds) * per + b / kXcds;
-    if (b / kXcds >= per || id >= tiles)
+    const int xcd = b % kXcds;
+    int64_t slot = b / kXcds;
+    int64_t tiles = (int64_t)whole * pt;
+    int64_t per = (tiles + kXcds - 1) / kXcds;
+    bool small = false;
+    int total = whole;
+    if (SPLIT && slot >= per) {
+        slot -= per;
+        total = part;
+        tiles = (int64_t)part * pt;
+        per = (tiles + kXcds - 1) / kXcds;
+        small = true;
+    }
+    const int64_t id = xcd * per + slot;
+    if (slot >= per || id >= tiles)
         return false;
     const int64_t grp = id / ((int64_t)GQ * pt);
     const int rem = (int)(id - grp * GQ * pt);
@@ -160,15 +186,17 @@ __device__ __forceinline__ bool find_tile(const ExpertRows &r, int pt, int b, Ti
     for (int e0 = 0; e0 < r.n; e0 += kWave) {
         int off = 0;
         const int c = rows_of(r, e0 + lane, off);
-        const int nt = (c + TQ - 1) / TQ;
+        const int nt = row_tiles<TQ, SPLIT>(c, small);
         const int incl = wave_inclusive_scan(nt) + before;
         const uint64_t past = __ballot(incl > q);
         if (past != 0) {
             const int win = __builtin_ctzll(past);
+            const int rows = __builtin_amdgcn_readlane(c, win);
             t.expert = e0 + win;
-            t.q = q - (__builtin_amdgcn_readlane(incl, win) - __builtin_amdgcn_readlane(nt, win));
+            t.q = small ? rows / TQ
+                        : q - (__builtin_amdgcn_readlane(incl, win) - __builtin_amdgcn_readlane(nt, win));
             t.row0 = __builtin_amdgcn_readlane(off, win) + t.q * TQ;
-            t.rows = __builtin_amdgcn_readlane(c, win) - t.q * TQ;
+            t.rows = rows - t.q * TQ;
             return true;
         }
         before = __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -182,8 +210,12 @@ inline int64_t most_row_tiles(int64_t rows, int n, int tq)
     return rows / tq + (rows < n ? rows : n);
 }
 
-// Workgroups for `tiles` tiles at most (a multiple of the XCDs).
-inline int64_t tile_blocks(int64_t tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
+// Workgroups for `tiles` tiles at most: a multiple of the XCDs, and one more
+// for each where whole and small tiles are rounded up apart.
+inline int64_t tile_blocks(int64_t tiles, bool split = false)
+{
+    return tiles == 0 ? 0 : ((tiles + kXcds - 1) / kXcds + split) * kXcds;
+}
 
 // ---------------------------------------------------------------- activation
 __device__ __forceinline__ float sigmoid32(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
