@@ -392,16 +392,12 @@ __global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
     Tile t;
     if constexpr (OP == kWgrad) {
-        // every expert has pt * qt tiles; an XCD gets neighbours
-        const int tiles = a.pt * a.qt, per = (tiles + kXcds - 1) / kXcds;
-        const int b = blockIdx.x, slots = per * kXcds;
-        t.expert = b / slots;
-        const int local = b - t.expert * slots;
-        const int id = local % kXcds * per + local / kXcds;
-        if (id >= tiles)
+        const int64_t tiles = (int64_t)a.pt * a.qt;   // of every expert
+        int64_t id, slots;
+        if (!spread(tiles * a.r.n, blockIdx.x % kXcds, blockIdx.x / kXcds, id, slots))
             return;
-        t.p = id % a.pt;
-        t.q = id / a.pt;
+        t.expert = (int)(id / tiles);
+        place(id - t.expert * tiles, a.qt, a.pt, t.p, t.q);
         t.row0 = 0;
         t.sum = uniform(rows_of(a.r, t.expert, t.row0));
         t.row0 = uniform(t.row0);
@@ -431,9 +427,9 @@ hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
     int64_t blocks;
     if (OP == kWgrad) {
         a.qt = (a.nq + TQ - 1) / TQ;
-        blocks = rows_or_n * tile_blocks((int64_t)a.pt * a.qt);
+        blocks = tile_blocks(rows_or_n * a.pt * a.qt);
     } else {
-        blocks = tile_blocks(most_row_tiles(rows_or_n, a.r.n, TQ) * a.pt, Kernel<OP, TP, TQ, BK, S, WP, WQ>::kDeep);
+        blocks = tile_blocks(most_row_tiles(rows_or_n, a.r.n, TQ) * a.pt);
     }
     if (blocks == 0)
         return hipSuccess;

@@ -138,19 +138,53 @@ template <int TQ, bool SPLIT> __device__ __forceinline__ int row_tiles(int c, bo
     return small ? rem > 0 && rem <= TQ / 2 : c / TQ + (rem > TQ / 2);
 }
 
+// Which of `tiles` tiles an XCD's workgroup number `slot` computes; false when
+// none is left for it. `slots` receives the workgroups that every XCD needs
+// for all of them.
+//
+// Neighbours in the order of tiles share operands. They are handed out in
+// rounds of about 256, one tile a CU, in which every XCD takes a run of
+// neighbours: those share what they read through the XCD's L2, and the runs
+// of one round through the memory-side cache (256 MB), which rows and weights
+// of a whole batch would not fit. A contiguous eighth of all tiles per XCD
+// instead spreads a round over the whole batch and read about twice as much
+// from HBM (32768 rows, one matrix of 4096 x 7168: the copies alone took 1310
+// us that way, against 1155 us for half as many rows of tiles at a time).
+__device__ __forceinline__ bool spread(int64_t tiles, int xcd, int64_t slot, int64_t &id, int64_t &slots)
+{
+    constexpr int kRound = 256;
+    const int64_t rounds = (tiles + kRound - 1) / kRound;
+    const int64_t run = rounds == 0 ? 0 : (tiles + kXcds * rounds - 1) / (kXcds * rounds);
+    slots = rounds * run;
+    if (slot >= slots)
+        return false;
+    const int64_t round = slot / run;
+    id = (round * kXcds + xcd) * run + slot - round * run;
+    return id < tiles;
+}
+
+// Tile `id` of `total` row tiles by pt column tiles, in the order of tiles:
+// GQ row tiles side by side, column after column.
+__device__ __forceinline__ void place(int64_t id, int total, int pt, int &p, int &q)
+{
+    constexpr int GQ = 8;
+    const int64_t grp = id / ((int64_t)GQ * pt);
+    const int rem = (int)(id - grp * GQ * pt);
+    const int q0 = (int)grp * GQ;
+    const int gq = total - q0 < GQ ? total - q0 : GQ;
+    p = rem / gq;
+    q = q0 + rem - p * gq;
+}
+
 // Tile of workgroup `b` for products whose row tiles are ragged: expert e has
 // ceil(rows / TQ) row tiles with pt column tiles each. Consecutive workgroups
-// run on different XCDs, so each XCD gets a contiguous eighth of the tiles
-// that there are; in it, GQ row tiles by GP = 4 column tiles are neighbours,
-// which share what they read through the XCD's L2. Small tiles come after all
-// others: they fill the last round of workgroups, which whole tiles would
-// leave mostly idle (32768 rows on 16 experts: 136 to 144 row tiles of 256,
-// where 128 would do). Every wave computes the same. False when there is no
-// tile for this workgroup.
+// run on different XCDs. Small tiles come after all others: they fill the
+// last round of workgroups, which whole tiles would leave mostly idle (32768
+// rows on 16 experts: 136 to 144 row tiles of 256, where 128 would do). Every
+// wave computes the same. False when there is no tile for this workgroup.
 template <int TQ, bool SPLIT>
 __device__ __forceinline__ bool find_tile(const ExpertRows &r, int pt, int b, Tile &t)
 {
-    constexpr int GQ = 8;
     const int lane = lane_id();
     int whole = 0, part = 0;
     for (int e0 = 0; e0 < r.n; e0 += kWave) {
@@ -160,28 +194,16 @@ __device__ __forceinline__ bool find_tile(const ExpertRows &r, int pt, int b, Ti
         if (SPLIT)
             part += __popcll(__ballot(row_tiles<TQ, SPLIT>(c, true) > 0));
     }
-    const int xcd = b % kXcds;
-    int64_t slot = b / kXcds;
-    int64_t tiles = (int64_t)whole * pt;
-    int64_t per = (tiles + kXcds - 1) / kXcds;
+    int64_t slot = b / kXcds, id, slots;
     bool small = false;
-    int total = whole;
-    if (SPLIT && slot >= per) {
-        slot -= per;
-        total = part;
-        tiles = (int64_t)part * pt;
-        per = (tiles + kXcds - 1) / kXcds;
+    if (!spread((int64_t)whole * pt, b % kXcds, slot, id, slots)) {
+        slot -= slots;
         small = true;
+        if (!SPLIT || slot < 0 || !spread((int64_t)part * pt, b % kXcds, slot, id, slots))
+            return false;
     }
-    const int64_t id = xcd * per + slot;
-    if (slot >= per || id >= tiles)
-        return false;
-    const int64_t grp = id / ((int64_t)GQ * pt);
-    const int rem = (int)(id - grp * GQ * pt);
-    const int q0 = (int)grp * GQ;
-    const int gq = total - q0 < GQ ? total - q0 : GQ;
-    t.p = rem / gq;
-    const int q = q0 + rem - t.p * gq;
+    int q;
+    place(id, small ? part : whole, pt, t.p, q);
     int before = 0;
     for (int e0 = 0; e0 < r.n; e0 += kWave) {
         int off = 0;
@@ -210,11 +232,11 @@ inline int64_t most_row_tiles(int64_t rows, int n, int tq)
     return rows / tq + (rows < n ? rows : n);
 }
 
-// Workgroups for `tiles` tiles at most: a multiple of the XCDs, and one more
-// for each where whole and small tiles are rounded up apart.
-inline int64_t tile_blocks(int64_t tiles, bool split = false)
+// Workgroups for `tiles` tiles at most, whole and small ones handed out apart
+// (spread: at most tiles / 8 + tiles / 256 + 2 an XCD for each kind).
+inline int64_t tile_blocks(int64_t tiles)
 {
-    return tiles == 0 ? 0 : ((tiles + kXcds - 1) / kXcds + split) * kXcds;
+    return tiles == 0 ? 0 : (tiles / kXcds + tiles / 256 + 4) * kXcds;
 }
 
 // ---------------------------------------------------------------- activation
