@@ -49,6 +49,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kSCopies = (kScales + kWaves - 1) / kWaves;
     static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
     static constexpr int kLds = S * kBuf;
+    static constexpr int kLag = 3;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!GLU || NI % 2 == 0, "gate and up fragments pair up in a wave");
     static_assert(!FP8OUT || PC % 128 == 0, "a tile holds whole scale blocks");
@@ -75,13 +76,10 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     }
     static __device__ __forceinline__ int q_key(int r) { return (r & 3) | (((r >> 2) & 1) << 2); }
 
-    static __device__ __forceinline__ void run(const Args &a, char *smem)
+    static __device__ __forceinline__ void run(const Args &a, const Tile &t, char *smem)
     {
         const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
         const int lane = lane_id(), m = lane & 15, g = lane >> 4;
-        Tile t;
-        if (!find_tile<TQ, false>(a.r, a.pt, blockIdx.x, t))
-            return;
         const int blocks = a.sum / 128, steps = (blocks + SUBS - 1) / SUBS;
         const int col0 = t.p * PC;
         const int mat_rows = GLU ? 2 * a.np : a.np, qrows = min(t.rows, TQ);
@@ -183,8 +181,18 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
 #pragma unroll
             for (int s = 0; s < SUBS; ++s) {
                 const uint32_t ps = at + kPBytes + kQBytes + s * (kPScale + kQScale) * 256, qs = ps + kPScale * 256;
-                i32x8 pf[NI];
+                i32x8 pf[NI], qf[2];
                 int sp[NI];
+                float sq[2];
+                auto read_q = [&](int j) {
+                    const int r = wq * (TQ / WQ) + j * 16 + m;
+                    const uint32_t row = at + kPBytes + r * kQRow;
+                    const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
+                    const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
+                    qf[j & 1] = i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    sq[j & 1] = lds_read<float>(qs + r * 4);
+                };
+                read_q(0);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int r = p_row(wp, i, m);
@@ -192,23 +200,28 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
                     pf[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
                     sp[i] = lds_read<uint8_t>(ps + r * 4 + g);
                 }
+                // A block's product is scaled and added three instructions
+                // after its own, which covers its latency.
+                f32x4 d[kLag + 1];
+                float ds[kLag + 1];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int r = wq * (TQ / WQ) + j * 16 + m;
-                    const uint32_t row = at + kPBytes + r * kQRow;
-                    const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
-                    const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
-                    const i32x8 qf = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    const float sq = lds_read<float>(qs + r * 4);
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
+                for (int x = 0; x < NI * NJ + kLag; ++x) {
+                    const int i = x % NI, j = x / NI;
+                    if (x < NI * NJ) {
+                        if (i == 0 && j + 1 < NJ)
+                            read_q(j + 1);
                         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf, zero, 4, 0, 0, sp[i],
-                                                                                         0, 127);
+                        d[x % (kLag + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf[j & 1], zero, 4, 0,
+                                                                                            0, sp[i], 0, 127);
+                        ds[x % (kLag + 1)] = sq[j & 1];
+                    }
+                    if (x >= kLag) {
+                        const int y = x - kLag, yi = y % NI, yj = y / NI, k = y % (kLag + 1);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            acc[i][j][q] = __builtin_fmaf(d[q], sq, acc[i][j][q]);
+                            acc[yi][yj][q] = __builtin_fmaf(d[k][q], ds[k], acc[yi][yj][q]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             buf = buf + 1 == S ? 0 : buf + 1;
@@ -299,7 +312,20 @@ __global__ __launch_bounds__(WP *WQ *kWave) void mx_kernel(Args a)
 {
     using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
-    K::run(a, smem);
+    constexpr bool kSplit = TQ == 256;   // the large tiles carry smaller ones for an expert's last rows
+    Tile t;
+    if (!find_tile<TQ, kSplit>(a.r, a.pt, blockIdx.x, t))
+        return;
+    if constexpr (kSplit) {
+        if (t.rows <= TQ / 4)
+            Kernel<GLU, FP8OUT, TP, TQ / 4, SUBS, S, WP, WQ>::run(a, t, smem);
+        else if (t.rows <= TQ / 2)
+            Kernel<GLU, FP8OUT, TP, TQ / 2, SUBS, S, WP, WQ>::run(a, t, smem);
+        else
+            K::run(a, t, smem);
+    } else {
+        K::run(a, t, smem);
+    }
 }
 
 template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ>
@@ -321,7 +347,7 @@ template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stre
 {
     const int64_t avg = a.r.num_rows / a.r.n;
     if (avg > 96)
-        return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 2>(a, stream);
+        return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 4>(a, stream);
     constexpr int TP = GLU && FP8OUT ? 256 : 128;
     if (avg > 16)
         return start<GLU, FP8OUT, TP, 64, 2, 3, 4, 1>(a, stream);

@@ -167,7 +167,7 @@ __device__ __forceinline__ bool spread(int64_t tiles, int xcd, int64_t slot, int
 // GQ row tiles side by side, column after column.
 __device__ __forceinline__ void place(int64_t id, int total, int pt, int &p, int &q)
 {
-    constexpr int GQ = 8;
+    constexpr int GQ = 4;
     const int64_t grp = id / ((int64_t)GQ * pt);
     const int rem = (int)(id - grp * GQ * pt);
     const int q0 = (int)grp * GQ;
