@@ -58,8 +58,8 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     static constexpr int GI = kPCols ? 1 : kHalf % 4 == 0 ? 4 : kHalf % 2 == 0 ? 2 : 1;
     static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
-    static constexpr int kLds = S * (kPBytes + kQBytes);
     static constexpr bool kDeep = S == 2;
+    static constexpr int kLds = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
 
@@ -187,18 +187,8 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
                 }
             }
         };
-        auto copy = [&](int c, uint32_t at) {
-            if (c < kPCopies)
-                copy16_to_lds(at + (wave * kPCopies + c) * 1024, rp, p_off[c]);
-            else
-                copy16_to_lds(at + kPBytes + (wave * kQCopies + c - kPCopies) * 1024, rq, q_off[c - kPCopies]);
-        };
-        auto issue = [&](int step, int buf) {
-            aim(step);
-#pragma unroll
-            for (int c = 0; c < kPCopies + kQCopies; ++c)
-                copy(c, lds + (uint32_t)buf * (kPBytes + kQBytes));
-        };
+        auto copy_p = [&](int c, uint32_t at) { copy16_to_lds(at + (wave * kPCopies + c) * 1024, rp, p_off[c]); };
+        auto copy_q = [&](int c, uint32_t at) { copy16_to_lds(at + (wave * kQCopies + c) * 1024, rq, q_off[c]); };
         auto read_p = [&](uint32_t at, int i, int s) {
             if constexpr (kPCols)
                 return read_cols<TP>(at, wp * (TP / WP) + i * 16, s);
@@ -207,9 +197,9 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         };
         auto read_q = [&](uint32_t at, int j, int s) {
             if constexpr (kQCols)
-                return read_cols<TQ>(at + kPBytes, wq * (TQ / WQ) + j * 16, s);
+                return read_cols<TQ>(at, wq * (TQ / WQ) + j * 16, s);
             else
-                return read_rows<QK>(at + kPBytes, wq * (TQ / WQ) + j * 16 + m, s);
+                return read_rows<QK>(at, wq * (TQ / WQ) + j * 16 + m, s);
         };
 
         f32x4 acc[NI][NJ];
@@ -220,63 +210,96 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
         if constexpr (kDeep) {
-            // Two buffers, and two sets of fragments in registers: while one
-            // half of a step (32 of the sum) is multiplied, the next half's
-            // fragments are read. The buffer of a step is free for the copies
-            // of the step after next as soon as its second half is read, and
-            // one meeting of the waves per step, between the halves, orders
-            // both that and the arrival of the next step.
+            // Two sets of fragments in registers: while one half of a step (32
+            // of the sum) is multiplied, the next half's fragments are read.
+            // The buffers of a step are free as soon as its second half is
+            // read; one meeting of the waves per step, between the halves,
+            // orders that and the arrival of the next step. P has three
+            // buffers and Q two (160 KB together), so that P's copies for the
+            // step after next go out in the first half and Q's in the second:
+            // all in one half would ask for more than a CU's 64 bytes a cycle.
             static_assert(S == 2 && BK == 64, "");
-            constexpr uint32_t kBuf = kPBytes + kQBytes;
-            constexpr int kCopies = kPCopies + kQCopies, kReads = NI + NJ;
+            constexpr int kReads = NI + NJ;
             // reads and copies before each of the NI rounds of NJ instructions
-            constexpr int kReadsPer = (kReads + NI - 2) / (NI - 1), kCopiesPer = (kCopies + NI - 1) / NI;
+            // (transposing reads are twice as many, and spread further)
+            constexpr int kReadsPer = kQCols ? (kReads + NI - 2) / (NI - 1) : (kReads + 1) / 2;
+            constexpr int kPPer = (kPCopies + NI - 1) / NI, kQPer = (kQCopies + NI - 1) / NI;
             bf16x8 pf[2][NI], qf[2][NJ];
-            auto read = [&](int set, uint32_t at, int c) {
+            auto read = [&](int set, uint32_t p_at, uint32_t q_at, int c) {
                 if (c < NJ)
-                    qf[set][c] = read_q(at, c, set);
+                    qf[set][c] = read_q(q_at, c, set);
                 else
-                    pf[set][c - NJ] = read_p(at, c - NJ, set);
+                    pf[set][c - NJ] = read_p(p_at, c - NJ, set);
             };
-            issue(0, 0);
-            issue(1, 1);
-            wait_copies<kCopies>();
+            const uint32_t lq = lds + 3 * kPBytes;
+            uint32_t p0 = lds, p1 = lds + kPBytes, p2 = lds + 2 * kPBytes;   // this step's, the next, the one after
+            uint32_t q0 = lq, q1 = lq + kQBytes;
+            aim(0);
+#pragma unroll
+            for (int c = 0; c < kPCopies; ++c)
+                copy_p(c, p0);
+#pragma unroll
+            for (int c = 0; c < kQCopies; ++c)
+                copy_q(c, q0);
+            aim(1);
+#pragma unroll
+            for (int c = 0; c < kPCopies; ++c)
+                copy_p(c, p1);
+#pragma unroll
+            for (int c = 0; c < kQCopies; ++c)
+                copy_q(c, q1);
+            wait_copies<kPCopies + kQCopies>();
 #pragma unroll
             for (int c = 0; c < kReads; ++c)
-                read(0, lds, c);
-            uint32_t at = lds, next = lds + kBuf;
+                read(0, p0, q0, c);
             for (int step = 0; step < steps; ++step) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-#pragma unroll
-                    for (int c = i * kReadsPer; c < (i + 1) * kReadsPer && c < kReads; ++c)
-                        read(1, at, c);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        mfma_in_place(acc[i][j], pf[0][i], qf[0][j]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                wait_copies<0>();
                 aim(step + 2);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
 #pragma unroll
                     for (int c = i * kReadsPer; c < (i + 1) * kReadsPer && c < kReads; ++c)
-                        read(0, next, c);
+                        read(1, p0, q0, c);
 #pragma unroll
-                    for (int c = i * kCopiesPer; c < (i + 1) * kCopiesPer && c < kCopies; ++c)
-                        copy(c, at);
+                    for (int c = i * kPPer; c < (i + 1) * kPPer && c < kPCopies; ++c)
+                        copy_p(c, p2);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        mfma_in_place(acc[i][j], pf[0][i], qf[0][j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                wait_copies<kPCopies>();   // all but the ones just made
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+#pragma unroll
+                    for (int c = i * kReadsPer; c < (i + 1) * kReadsPer && c < kReads; ++c)
+                        read(0, p1, q1, c);
+#pragma unroll
+                    for (int c = i * kQPer; c < (i + 1) * kQPer && c < kQCopies; ++c)
+                        copy_q(c, q0);
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
                         mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                const uint32_t swap = at;
-                at = next;
-                next = swap;
+                const uint32_t free_p = p0, free_q = q0;
+                p0 = p1;
+                p1 = p2;
+                p2 = free_p;
+                q0 = q1;
+                q1 = free_q;
             }
             mfma_settle();
         } else {
+            auto issue = [&](int step, int buf) {
+                const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
+                aim(step);
+#pragma unroll
+                for (int c = 0; c < kPCopies; ++c)
+                    copy_p(c, at);
+#pragma unroll
+                for (int c = 0; c < kQCopies; ++c)
+                    copy_q(c, at + kPBytes);
+            };
 #pragma unroll
             for (int s = 0; s < S - 1; ++s)
                 issue(s, s);
@@ -295,7 +318,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
                         pf[i] = read_p(at, i, s);
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
-                        qf[j] = read_q(at, j, s);
+                        qf[j] = read_q(at + kPBytes, j, s);
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
 #pragma unroll

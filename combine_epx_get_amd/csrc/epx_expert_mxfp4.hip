@@ -117,49 +117,41 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
         }
         const uint32_t lds = lds_offset(smem);
 
-        auto issue = [&](int step, int buf) {
+        // descriptors of the operands' parts in a step (empty past the last)
+        i32x4 rp, rq, rps, rqs;
+        int left = 0;   // blocks from the step's first to the sum's end
+        auto aim = [&](int step) {
             const bool live = step < steps;
             const int b0 = step * SUBS;   // first block of 128
-            const uint32_t at = lds + (uint32_t)buf * kBuf;
-            const i32x4 rp = buffer_of(pb + (int64_t)b0 * 64, live ? p_bytes - (uint32_t)b0 * 64u : 0u);
-            const i32x4 rq = buffer_of(qb + (int64_t)b0 * 128, live ? q_bytes - (uint32_t)b0 * 128u : 0u);
-            const i32x4 rps = buffer_of(psb + (int64_t)b0 * 4, live ? ps_bytes - (uint32_t)b0 * 4u : 0u);
-            const i32x4 rqs = buffer_of(qsb + (int64_t)b0 * 4, live ? qs_bytes - (uint32_t)b0 * 4u : 0u);
-            // a last step of fewer blocks: what lies past the sum's end would
-            // be the next row's first
-            const bool tail = SUBS > 1 && live && b0 + SUBS > blocks;
-#pragma unroll
-            for (int c = 0; c < kPCopies; ++c) {
+            rp = buffer_of(pb + (int64_t)b0 * 64, live ? p_bytes - (uint32_t)b0 * 64u : 0u);
+            rq = buffer_of(qb + (int64_t)b0 * 128, live ? q_bytes - (uint32_t)b0 * 128u : 0u);
+            rps = buffer_of(psb + (int64_t)b0 * 4, live ? ps_bytes - (uint32_t)b0 * 4u : 0u);
+            rqs = buffer_of(qsb + (int64_t)b0 * 4, live ? qs_bytes - (uint32_t)b0 * 4u : 0u);
+            left = blocks - b0;
+        };
+        // A last step of fewer blocks: what lies past the sum's end would be
+        // the next row's first.
+        auto copy = [&](int c, uint32_t at) {
+            if (c < kPCopies) {
                 const int inst = wave * kPCopies + c;
-                uint32_t o = p_off[c];
-                if (tail) {
-                    constexpr int lanes = kPRow / 16;
-                    const int r = inst * (64 / lanes) + lane / lanes;
-                    if ((((lane % lanes) ^ p_key(r)) >> 2) + b0 >= blocks)
-                        o = kOutside;
-                }
-                copy16_to_lds(at + inst * 1024, rp, o);
-            }
-#pragma unroll
-            for (int c = 0; c < kQCopies; ++c) {
-                const int inst = wave * kQCopies + c;
-                uint32_t o = q_off[c];
-                if (tail) {
-                    constexpr int lanes = kQRow / 16;
-                    const int r = inst * (64 / lanes) + lane / lanes;
-                    if ((((lane % lanes) ^ q_key(r)) >> 3) + b0 >= blocks)
-                        o = kOutside;
-                }
-                copy16_to_lds(at + kPBytes + inst * 1024, rq, o);
-            }
-#pragma unroll
-            for (int c = 0; c < kSCopies; ++c) {
-                const int inst = wave * kSCopies + c, sub = inst / (kPScale + kQScale);
+                constexpr int lanes = kPRow / 16;
+                const int r = inst * (64 / lanes) + lane / lanes;
+                const bool out = SUBS > 1 && (((lane % lanes) ^ p_key(r)) >> 2) >= left;
+                copy16_to_lds(at + inst * 1024, rp, out ? kOutside : p_off[c]);
+            } else if (c < kPCopies + kQCopies) {
+                const int d = c - kPCopies, inst = wave * kQCopies + d;
+                constexpr int lanes = kQRow / 16;
+                const int r = inst * (64 / lanes) + lane / lanes;
+                const bool out = SUBS > 1 && (((lane % lanes) ^ q_key(r)) >> 3) >= left;
+                copy16_to_lds(at + kPBytes + inst * 1024, rq, out ? kOutside : q_off[d]);
+            } else {
+                const int d = c - kPCopies - kQCopies, inst = wave * kSCopies + d, sub = inst / (kPScale + kQScale);
                 const bool is_p = inst % (kPScale + kQScale) < kPScale;
                 copy4_to_lds(at + kPBytes + kQBytes + inst * 256, is_p ? rps : rqs,
-                             tail && b0 + sub >= blocks ? kOutside : s_off[c]);
+                             SUBS > 1 && sub >= left ? kOutside : s_off[d]);
             }
         };
+        constexpr int kCopies = kPCopies + kQCopies + kSCopies;
 
         f32x4 acc[NI][NJ];
 #pragma unroll
@@ -169,14 +161,27 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s)
-            issue(s, s);
+        for (int s = 0; s < S - 1; ++s) {
+            aim(s);
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c)
+                copy(c, lds + (uint32_t)s * kBuf);
+        }
         int buf = 0;
         for (int step = 0; step < steps; ++step) {
-            wait_copies<(S - 2) * (kPCopies + kQCopies + kSCopies)>();
+            wait_copies<(S - 2) * kCopies>();
             int into = buf + S - 1;
             into = into >= S ? into - S : into;
-            issue(step + S - 1, into);
+            const uint32_t to = lds + (uint32_t)into * kBuf;
+            aim(step + S - 1);
+            // copies are spread over the step's instructions where there are
+            // enough of them; small tiles, which wait for memory, make them first
+            constexpr int kSpread = SUBS * NI * NJ >= 2 * kCopies ? SUBS * NI * NJ / kCopies : 0;
+            if (kSpread == 0) {
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c)
+                    copy(c, to);
+            }
             const uint32_t at = lds + (uint32_t)buf * kBuf;
 #pragma unroll
             for (int s = 0; s < SUBS; ++s) {
@@ -208,6 +213,9 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
                 for (int x = 0; x < NI * NJ + kLag; ++x) {
                     const int i = x % NI, j = x / NI;
                     if (x < NI * NJ) {
+                        const int at_x = s * NI * NJ + x;
+                        if (kSpread > 0 && at_x % (kSpread ? kSpread : 1) == 0 && at_x / (kSpread ? kSpread : 1) < kCopies)
+                            copy(at_x / (kSpread ? kSpread : 1), to);
                         if (i == 0 && j + 1 < NJ)
                             read_q(j + 1);
                         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
