@@ -24,7 +24,7 @@
 namespace epx {
 namespace {
 
-enum Op { kForward, kForwardGlu, kDgrad, kDgradGlu, kWgrad };
+enum Op { kForward, kForwardGlu, kDgrad, kDgradGlu, kWgrad, kWgradF32 };
 
 struct Args {
     ExpertRows r;
@@ -35,7 +35,7 @@ struct Args {
     const uint16_t *preact_in;
     uint16_t *preact_out;
     void *out;
-    int32_t f32, accumulate;
+    int32_t accumulate;
 };
 
 // Which 16-byte chunk of a row a chunk is kept at: exclusive or with these.
@@ -49,13 +49,14 @@ __host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v
 template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     static constexpr bool kGlu = OP == kForwardGlu;
     static constexpr bool kPCols = OP >= kDgrad;     // P's sum index is the row in memory
-    static constexpr bool kQCols = OP == kWgrad;
+    static constexpr bool kWeights = OP >= kWgrad;
+    static constexpr bool kQCols = kWeights;
     static constexpr int kWaves = WP * WQ, kThreads = kWaves * kWave;
     static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
-    // P fragments whose results are merged: a lane then has 4 * GI
-    // consecutive columns
+    // P fragments whose rows are read such that a lane has 4 * GI consecutive
+    // columns of them
     static constexpr int kHalf = kGlu ? NI / 2 : NI;
-    static constexpr int GI = kPCols ? 1 : kHalf % 4 == 0 ? 4 : kHalf % 2 == 0 ? 2 : 1;
+    static constexpr int GI = kPCols || kHalf % 2 != 0 ? 1 : 2;
     static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
     static constexpr bool kDeep = S == 2;
@@ -126,7 +127,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         const int m = lane_id() & 15, g = lane_id() >> 4;
         constexpr int PK = 2 + log2i(GI), QK = 2;   // row_key bits
 
-        const int sum = OP == kWgrad ? t.sum : a.sum;
+        const int sum = kWeights ? t.sum : a.sum;
         const int steps = (sum + BK - 1) / BK;
         constexpr int PC = kGlu ? TP / 2 : TP;   // output columns of a tile
         const int col0 = t.p * PC;
@@ -134,7 +135,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         // operand bases and, for operands whose sum index is the memory row, their last byte
         const char *pb, *qb;
         uint32_t p_bytes = 0, q_bytes = 0;
-        if constexpr (OP == kWgrad) {
+        if constexpr (kWeights) {
             pb = a.p + ((int64_t)t.row0 * a.np + col0) * 2;
             qb = a.q + ((int64_t)t.row0 * a.nq + t.q * TQ) * 2;
         } else if constexpr (kPCols) {
@@ -330,76 +331,71 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         }
         drain_copies();
 
-        // results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
-        // columns 4 g .. 4 g + 3 of fragment i, merged over GI fragments
-        constexpr int NG = kHalf / GI;
+        // Results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
+        // columns 4 g .. 4 g + 3 of fragment i. Two fragments are neighbours
+        // already where P's rows are read that way (GI), and are merged here
+        // otherwise, so that the lanes of a write are neighbours in 64 bytes
+        // of a row (float32 results are so as they are).
+        constexpr bool kMerge = kPCols && OP != kWgradF32 && NI % 2 == 0;
+        constexpr int W = kMerge ? 2 : GI, NG = kHalf / W;
+        if constexpr (kMerge) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    merge_columns(acc[2 * n][j], acc[2 * n + 1][j]);
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int r = wq * (TQ / WQ) + j * 16 + m;
-            if constexpr (OP == kWgrad) {
-                const int n = t.q * TQ + r;
-                if (n >= a.nq)
-                    continue;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int c = col0 + wp * (TP / WP) + i * 16 + 4 * g;
-                    if (c >= a.np)
-                        continue;
-                    const int64_t o = ((int64_t)t.expert * a.nq + n) * a.np + c;
-                    if (a.f32) {
-                        f32x4 *d = (f32x4 *)((float *)a.out + o);
-                        *d = a.accumulate ? *d + acc[i][j] : acc[i][j];
-                    } else {
-                        *(u32x2 *)((uint16_t *)a.out + o) =
-                            u32x2{pack2(acc[i][j].x, acc[i][j].y), pack2(acc[i][j].z, acc[i][j].w)};
+            for (int n = 0; n < NG; ++n) {
+                const int c = col0 + wp * (PC / WP) + n * 16 * W + 4 * W * g;
+                Cols<4 * W> u, v;
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        u.v[4 * i + q] = acc[n * W + i][j][q];
+                        if constexpr (kGlu)
+                            v.v[4 * i + q] = acc[kHalf + n * W + i][j][q];
                     }
-                }
-            } else {
-                if (r >= t.rows)
-                    continue;
-                const int64_t row = t.row0 + r;
-#pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    Cols<4 * GI> u, v;
-#pragma unroll
-                    for (int i = 0; i < GI; ++i)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            u.v[4 * i + q] = acc[n * GI + i][j][q];
-                            if constexpr (kGlu)
-                                v.v[4 * i + q] = acc[kHalf + n * GI + i][j][q];
-                        }
-                    const int c = col0 + wp * (PC / WP) + n * 16 * GI + 4 * GI * g;
-                    if constexpr (OP == kForward) {
-                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
-                    } else if constexpr (OP == kForwardGlu) {
+                if constexpr (kWeights) {
+                    const int row = t.q * TQ + r;
+                    if (row >= a.nq)
+                        continue;
+                    const int64_t o = ((int64_t)t.expert * a.nq + row) * a.np;
+                    if constexpr (OP == kWgradF32)
+                        store_f32((float *)a.out + o, c, a.np, u, a.accumulate);
+                    else
+                        store_bf16((uint16_t *)a.out + o, c, a.np, u);
+                } else {
+                    if (r >= t.rows)
+                        continue;
+                    const int64_t row = t.row0 + r;
+                    if constexpr (OP == kForwardGlu) {
                         if (a.preact_out) {
                             store_bf16(a.preact_out + row * 2 * a.np, c, a.np, u);
                             store_bf16(a.preact_out + row * 2 * a.np + a.np, c, a.np, v);
                         }
 #pragma unroll
-                        for (int q = 0; q < 4 * GI; ++q)
+                        for (int q = 0; q < 4 * W; ++q)
                             u.v[q] = swiglu(u.v[q], v.v[q]);
-                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
-                    } else if constexpr (OP == kDgrad) {
-                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
-                    } else {
-                        if (c >= a.np)
-                            continue;
-                        const uint16_t *pre = a.preact_in + row * 2 * a.np + c;
-                        const u32x2 gv = *(const u32x2 *)pre, uv = *(const u32x2 *)(pre + a.np);
-                        const float gate[4] = {bf16_lo(gv.x), bf16_hi(gv.x), bf16_lo(gv.y), bf16_hi(gv.y)};
-                        const float up[4] = {bf16_lo(uv.x), bf16_hi(uv.x), bf16_lo(uv.y), bf16_hi(uv.y)};
-                        Cols<4> dg, du;
+                    }
+                    if constexpr (OP == kDgradGlu) {
+                        const uint16_t *pre = a.preact_in + row * 2 * a.np;
+                        const Cols<4 * W> gate = load_bf16<4 * W>(pre, c, a.np), up = load_bf16<4 * W>(pre + a.np, c, a.np);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float s = sigmoid32(gate[q]);
-                            dg.v[q] = u.v[q] * up[q] * (s * (1.0f + gate[q] * (1.0f - s)));
-                            du.v[q] = u.v[q] * (gate[q] * s);
+                        for (int q = 0; q < 4 * W; ++q) {
+                            const float s = sigmoid32(gate.v[q]), d = u.v[q];
+                            u.v[q] = d * up.v[q] * (s * (1.0f + gate.v[q] * (1.0f - s)));
+                            v.v[q] = d * (gate.v[q] * s);
                         }
                         uint16_t *dx = (uint16_t *)a.out + row * 2 * a.np;
-                        store_bf16(dx, c, a.np, dg);
-                        store_bf16(dx + a.np, c, a.np, du);
+                        store_bf16(dx, c, a.np, u);
+                        store_bf16(dx + a.np, c, a.np, v);
+                    } else {
+                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
                     }
                 }
             }
@@ -414,7 +410,7 @@ __global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
     using K = Kernel<OP, TP, TQ, BK, S, WP, WQ>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
     Tile t;
-    if constexpr (OP == kWgrad) {
+    if constexpr (K::kWeights) {
         const int64_t tiles = (int64_t)a.pt * a.qt;   // of every expert
         int64_t id, slots;
         if (!spread(tiles * a.r.n, blockIdx.x % kXcds, blockIdx.x / kXcds, id, slots))
@@ -448,7 +444,7 @@ hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
     constexpr int PC = OP == kForwardGlu ? TP / 2 : TP;
     a.pt = (a.np + PC - 1) / PC;
     int64_t blocks;
-    if (OP == kWgrad) {
+    if (OP >= kWgrad) {
         a.qt = (a.nq + TQ - 1) / TQ;
         blocks = tile_blocks(rows_or_n * a.pt * a.qt);
     } else {
@@ -518,11 +514,12 @@ hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *
     a.np = inner;
     a.nq = width;
     a.out = dw;
-    a.f32 = f32;
     a.accumulate = accumulate;
     if ((int64_t)width * inner >= 2048 * 2048)
-        return start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
-    return start<kWgrad, 128, 128, 64, 3, 2, 2>(a, r.n, stream);
+        return f32 ? start<kWgradF32, 256, 256, 64, 2, 4, 2>(a, r.n, stream)
+                   : start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
+    return f32 ? start<kWgradF32, 128, 128, 64, 3, 2, 2>(a, r.n, stream)
+               : start<kWgrad, 128, 128, 64, 3, 2, 2>(a, r.n, stream);
 }
 
 }  // namespace epx

@@ -37,7 +37,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kWaves = WP * WQ;
     static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
     static constexpr int kHalf = GLU ? NI / 2 : NI;
-    static constexpr int GI = kHalf % 4 == 0 ? 4 : kHalf % 2 == 0 ? 2 : 1;
+    static constexpr int GI = kHalf % 2 == 0 ? 2 : 1;
     static constexpr int PC = GLU ? TP / 2 : TP;
     static constexpr int kPRow = 64 * SUBS, kQRow = 128 * SUBS;   // bytes of a row in LDS
     static constexpr int kPBytes = TP * kPRow, kQBytes = TQ * kQRow;

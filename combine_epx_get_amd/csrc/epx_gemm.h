@@ -239,6 +239,22 @@ inline int64_t tile_blocks(int64_t tiles)
     return tiles == 0 ? 0 : (tiles / kXcds + tiles / 256 + 4) * kXcds;
 }
 
+// From lane group g holding columns 4 g .. 4 g + 3 of each of two
+// neighbouring fragments to holding columns 8 g .. 8 g + 7 of the two: a write
+// of 16 bytes a lane is then one of 64 neighbouring bytes a row (bf16).
+__device__ __forceinline__ void merge_columns(f32x4 &a, f32x4 &b)
+{
+    typedef uint32_t u32p __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float aq = a[q], bq = b[q];
+        const u32p h = __builtin_amdgcn_permlane32_swap(__float_as_uint(aq), __float_as_uint(bq), false, false);
+        const u32p x = __builtin_amdgcn_permlane16_swap(h.x, h.y, false, false);
+        a[q] = __uint_as_float(x.x);
+        b[q] = __uint_as_float(x.y);
+    }
+}
+
 // ---------------------------------------------------------------- activation
 __device__ __forceinline__ float sigmoid32(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 __device__ __forceinline__ float swiglu(float gate, float up) { return gate * sigmoid32(gate) * up; }
@@ -262,6 +278,43 @@ __device__ __forceinline__ void store_bf16(uint16_t *row, int c, int width, cons
                 *(u32x4 *)(row + c + i) = u32x4{pack2(o.v[i], o.v[i + 1]), pack2(o.v[i + 2], o.v[i + 3]),
                                                 pack2(o.v[i + 4], o.v[i + 5]), pack2(o.v[i + 6], o.v[i + 7])};
     }
+}
+
+// The same of a float32 row, written or added.
+template <int N>
+__device__ __forceinline__ void store_f32(float *row, int c, int width, const Cols<N> &o, bool add)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        if (c + i < width) {
+            f32x4 *d = (f32x4 *)(row + c + i);
+            const f32x4 x = {o.v[i], o.v[i + 1], o.v[i + 2], o.v[i + 3]};
+            *d = add ? *d + x : x;
+        }
+}
+
+// Columns [c, c + N) of a bf16 row; 0 past its `width` columns.
+template <int N> __device__ __forceinline__ Cols<N> load_bf16(const uint16_t *row, int c, int width)
+{
+    Cols<N> o;
+    if constexpr (N == 4) {
+        const u32x2 v = c < width ? *(const u32x2 *)(row + c) : u32x2{0, 0};
+        o.v[0] = bf16_lo(v.x);
+        o.v[1] = bf16_hi(v.x);
+        o.v[2] = bf16_lo(v.y);
+        o.v[3] = bf16_hi(v.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const u32x4 v = c + i < width ? *(const u32x4 *)(row + c + i) : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                o.v[i + 2 * q] = bf16_lo(v[q]);
+                o.v[i + 2 * q + 1] = bf16_hi(v[q]);
+            }
+        }
+    }
+    return o;
 }
 
 }  // namespace epx
