@@ -59,7 +59,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     static constexpr int GI = kPCols || kHalf % 2 != 0 ? 1 : 2;
     static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
-    static constexpr bool kDeep = S == 2;
+    static constexpr bool kDeep = TP == 256;
     static constexpr int kLds = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
@@ -473,15 +473,26 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
     a.sum = inner;
     a.preact_out = (uint16_t *)preact;
     a.out = out;
-    const int64_t avg = r.num_rows / r.n;
-    if (avg > 96)
-        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
-                      : start<kForward, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
-    if (avg > 16)
-        return swiglu ? start<kForwardGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
-                      : start<kForward, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
-    return swiglu ? start<kForwardGlu, 128, 32, 64, 4, 4, 1>(a, r.num_rows, stream)
-                  : start<kForward, 128, 32, 64, 4, 4, 1>(a, r.num_rows, stream);
+    // Large tiles where they occupy the GPU and most experts have more than
+    // the 64 rows of the next size; that one above the 32 rows of the
+    // smallest (a tile more reads an expert's weights again), unless its
+    // tiles leave CUs idle. Measured, us, large / 64 rows / 32 rows, gated:
+    //   16 experts of 2048 x 7168, 16 rows each 156 / 157 / 157, 48 rows
+    //   159 / 159 / 198, 96 rows 167 / 219 / 283, 256 rows 215 / 403 / 554;
+    //   64 of 1024 x 2048, 16 rows 128 / 113 / 108, 64 rows 132 / 115 / 121,
+    //   128 rows 143 / 138 / 182, 192 rows 164 / 182 / 245;
+    //   16 of 512 x 1024 (64 to 128 large tiles), 16 rows 12.1 / 9.5 / 8.3, 128
+    //   rows 17.1 / 11.1 / 11.8, 384 rows 28.6 / 21.6 / 29.7;
+    //   8 of 2048 x 7168, 256 ragged rows: 106 / 82 / 113.
+    const int64_t rows = r.num_rows, n = r.n;
+    if (rows > 64 * n && tiles_of(r, 256, width, swiglu ? 128 : 256) >= 256)
+        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, rows, stream)
+                      : start<kForward, 256, 256, 64, 2, 4, 2>(a, rows, stream);
+    if (rows > 20 * n && tiles_of(r, 64, width, swiglu ? 64 : 128) >= 256)
+        return swiglu ? start<kForwardGlu, 128, 64, 64, 3, 4, 1>(a, rows, stream)
+                      : start<kForward, 128, 64, 64, 3, 4, 1>(a, rows, stream);
+    return swiglu ? start<kForwardGlu, 128, 32, 64, 4, 4, 1>(a, rows, stream)
+                  : start<kForward, 128, 32, 64, 4, 4, 1>(a, rows, stream);
 }
 
 hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *w, int32_t width,
@@ -495,12 +506,15 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     a.sum = width;
     a.preact_in = (const uint16_t *)preact;
     a.out = dx;
-    const int64_t avg = r.num_rows / r.n;
-    if (avg > 96)
+    // Measured, us, large / small tiles: 16 experts of 2048 x 7168, 16 rows
+    // each 84.5 / 87.1, 256 rows 131 / 198; 64 of 1024 x 2048, 16 rows 44.8 /
+    // 43.1, 96 rows 56 / 74; 16 of 512 x 1024 (64 to 128 large tiles), 256 rows
+    // 21.0 / 10.7, 384 rows 22.3 / 17.3.
+    if (tiles_of(r, 256, inner, 256) >= 256)
         return preact ? start<kDgradGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
-    return preact ? start<kDgradGlu, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream)
-                  : start<kDgrad, 128, 64, 64, 4, 4, 1>(a, r.num_rows, stream);
+    return preact ? start<kDgradGlu, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream)
+                  : start<kDgrad, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream);
 }
 
 hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *x, int32_t width,
@@ -515,11 +529,18 @@ hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *
     a.nq = width;
     a.out = dw;
     a.accumulate = accumulate;
-    if ((int64_t)width * inner >= 2048 * 2048)
+    // Large tiles for long sums and enough tiles; three workgroups of small
+    // ones share a CU, which covers the start and end of short sums. Measured,
+    // us, large / small: 16 experts of 2048 x 7168, 64 rows each 174 / 155
+    // (bf16), 213 / 185 (float32), 256 rows 263 / 243, 294 / 330, 1024 rows
+    // 519 / 569, 545 / 703; 64 of 1024 x 2048, 64 rows 105 / 85, 1024 rows
+    // 308 / 345; 8 of 512 x 1024 (64 large tiles), 1024 rows 31 / 20.
+    const int64_t tiles = (int64_t)((width + 255) / 256) * ((inner + 255) / 256) * r.n;
+    if (tiles >= 128 && r.num_rows >= 384 * (int64_t)r.n)
         return f32 ? start<kWgradF32, 256, 256, 64, 2, 4, 2>(a, r.n, stream)
                    : start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
-    return f32 ? start<kWgradF32, 128, 128, 64, 3, 2, 2>(a, r.n, stream)
-               : start<kWgrad, 128, 128, 64, 3, 2, 2>(a, r.n, stream);
+    return f32 ? start<kWgradF32, 128, 128, 32, 3, 2, 2>(a, r.n, stream)
+               : start<kWgrad, 128, 128, 32, 3, 2, 2>(a, r.n, stream);
 }
 
 }  // namespace epx

@@ -353,12 +353,19 @@ hipError_t start(Args a, hipStream_t stream)
 
 template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stream)
 {
-    const int64_t avg = a.r.num_rows / a.r.n;
-    if (avg > 96)
+    // As the bf16 products, with other borders. Measured, us, large / 64 rows
+    // / 32 rows, gated: 16 experts of 2048 x 7168, 16 rows each 51 / 56 / 45,
+    // 48 rows 52 / 60 / 69, 128 rows 74 / 113 / 134; 64 of 1024 x 2048, 32 rows
+    // 32 / 34 / 29, 48 rows 34 / 35 / 44; 16 of 512 x 1024 (64 to 128 large
+    // tiles), 64 rows 9.8 / 8.9 / 9.0, 192 rows 19.2 / 11.1 / 12.7, 384 rows
+    // 20.2 / 17.0 / 21.9.
+    const int64_t rows = a.r.num_rows, n = a.r.n;
+    if (rows > 28 * n && tiles_of(a.r, 256, a.np, GLU ? 128 : 256) >= 256)
         return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 4>(a, stream);
+    // fp8 rows out need whole scale blocks of 128 columns in a tile
     constexpr int TP = GLU && FP8OUT ? 256 : 128;
-    if (avg > 16)
-        return start<GLU, FP8OUT, TP, 64, 2, 3, 4, 1>(a, stream);
+    if (rows > 64 * n || (rows > 28 * n && tiles_of(a.r, 64, a.np, GLU ? TP / 2 : TP) >= 256))
+        return start<GLU, FP8OUT, TP, 64, 1, 4, 4, 1>(a, stream);
     return start<GLU, FP8OUT, TP, 32, 2, 3, 4, 1>(a, stream);
 }
 

@@ -255,6 +255,15 @@ __device__ __forceinline__ void merge_columns(f32x4 &a, f32x4 &b)
     }
 }
 
+// Tiles of `height` rows and `tile_columns` columns that a product has with
+// its experts equally full, each with a last tile half full.
+inline int64_t tiles_of(const ExpertRows &r, int height, int64_t columns, int tile_columns)
+{
+    const int64_t experts = r.n < r.num_rows ? r.n : r.num_rows;
+    const int64_t half_full = r.num_rows / height + experts / 2;
+    return (half_full > experts ? half_full : experts) * ((columns + tile_columns - 1) / tile_columns);
+}
+
 // ---------------------------------------------------------------- activation
 __device__ __forceinline__ float sigmoid32(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 __device__ __forceinline__ float swiglu(float gate, float up) { return gate * sigmoid32(gate) * up; }

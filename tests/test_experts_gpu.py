@@ -46,7 +46,8 @@ def untouched(t, off, cnt, name):
 
 
 # counts, gap between ranges, order of ranges in memory, width, inner. The
-# average rows per expert choose the kernel: up to 16, up to 96, above.
+# average rows per expert and the number of tiles choose the kernel; the large
+# ones need 256 tiles of 256 x 256 (the last three cases).
 CASES = [
     ("one row", [1], 0, None, 8, 8),
     ("one row each", [1, 1, 1, 1], 0, None, 40, 72),
@@ -62,6 +63,9 @@ CASES = [
     ("many experts", [i % 5 for i in range(200)], 0, None, 72, 64),
     ("more experts than lanes, large", [150 + (i * 37) % 90 for i in range(70)], 0, None, 64, 72),
     ("wide", [3, 2], 0, None, 4104, 24),
+    ("150 experts, every kind of last tile", [(i * 53) % 300 for i in range(150)], 1, None, 264, 520),
+    ("very wide", [700, 300], 0, [1, 0], 16392, 136),
+    ("very long sum", [700, 300], 2, None, 136, 16392),
 ]
 IDS = [c[0] for c in CASES]
 
@@ -137,20 +141,22 @@ def test_weight_gradient(epx, case, kind):
         ref.close(dw[e], want, bound, ref.BF16 if kind == "bf16" else 2.0 ** -24, ("dw", e))
 
 
-def test_large_matrices_weight_gradient(epx):
-    """The larger weight-gradient tiles (width * inner of 2^22 on), sizes that end inside them."""
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_large_tiles_weight_gradient(epx, dtype):
+    """The larger weight-gradient tiles (128 tiles and 384 rows an expert on average), sizes that end inside them."""
     g = gen(4)
-    cnt = [70, 0, 1, 130]
+    cnt = [400, 0, 901, 5, 1300]
     off, R = ref.ranges(cnt, 1)
-    N, K = 2056, 2064
+    N, K = 1032, 2056
     rows = make_rows(epx, off, cnt, R)
     dy, x = rand(g, R, N), rand(g, R, K)
-    dw = guard(len(cnt), N, K, dtype=torch.float32)
+    dw = guard(len(cnt), N, K, dtype=dtype)
     epx.epx_expert_gemm_wgrad(rows, dy, x, dw)
     torch.cuda.synchronize()
     for e, (o, c) in enumerate(zip(off, cnt)):
         a, v = dy[o:o + c].double(), x[o:o + c].double()
-        ref.close(dw[e], a.T @ v, a.abs().T @ v.abs() * (ref.SUM * max(c, 1)), 2.0 ** -24, ("dw", e))
+        ref.close(dw[e], a.T @ v, a.abs().T @ v.abs() * (ref.SUM * max(c, 1)),
+                  ref.BF16 if dtype == torch.bfloat16 else 2.0 ** -24, ("dw", e))
 
 
 def test_ranges_outside_the_buffers_count_as_empty(epx):

@@ -126,7 +126,9 @@ def test_product(epx, case, act):
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 @pytest.mark.parametrize("case", [("one", [1], 0, None, 128, 128), ("decode", [0, 3, 17, 1], 2, None, 384, 640),
                                   ("middle", [50, 0, 90, 64], 1, [2, 0, 1, 3], 256, 384),
-                                  ("large", [130, 257, 3], 0, None, 640, 256)], ids=lambda c: c[0])
+                                  ("more rows", [130, 257, 3], 0, None, 640, 256),
+                                  ("large tiles", [(i * 53) % 300 for i in range(150)], 1, None, 384, 256)],
+                         ids=lambda c: c[0])
 def test_product_to_fp8_rows(epx, case, act):
     name, cnt, gap, order, N, K = case
     off, R = ref.ranges(cnt, gap, order)
