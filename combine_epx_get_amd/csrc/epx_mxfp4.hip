@@ -27,15 +27,27 @@ __device__ __forceinline__ float e8m0(uint32_t b)
     return b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(b == 0 ? 0x00400000u : b << 23);
 }
 
-// A lane takes 8 values (16 bytes in, 4 bytes of codes out), four lanes a
-// block: reads and writes are contiguous over the wave.
-__global__ __launch_bounds__(256) void quantize_kernel(const u32x4 *__restrict__ x, int64_t nvec,
-                                                       uint32_t *__restrict__ codes,
-                                                       uint8_t *__restrict__ scales)
+// A lane takes 8 values (16 bytes of bf16, 4 bytes of codes), four lanes a
+// block: reads and writes are contiguous over the wave. kUnroll such pieces
+// of a lane are loaded before the first is converted.
+constexpr int kUnroll = 4, kThreads = 256;
+
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const u32x4 *__restrict__ x, int64_t nvec,
+                                                            uint32_t *__restrict__ codes,
+                                                            uint8_t *__restrict__ scales)
 {
-    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nvec; i += stride) {
-        const u32x4 v = x[i];
+    const int64_t base = (int64_t)blockIdx.x * kThreads * kUnroll + threadIdx.x;
+    u32x4 in[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (base + u * kThreads < nvec)
+            in[u] = __builtin_nontemporal_load(x + base + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t i = base + u * kThreads;
+        if (i >= nvec)
+            return;   // whole blocks of four lanes: nvec is a multiple of 4
+        const u32x4 v = in[u];
         uint32_t m = max_magnitude(max_magnitude(max_magnitude(max_magnitude(0, v.x), v.y), v.z), v.w);
         m = max(m, (uint32_t)__shfl_xor((int)m, 1, 4));
         m = max(m, (uint32_t)__shfl_xor((int)m, 2, 4));
@@ -63,8 +75,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const u32x4 *__restrict__
     }
 }
 
-// bf16 bits of a code's magnitude times 2: codes 0..7 stand for 0, 1, 2, 3,
-// 4, 6, 8, 12 halves.
+// A code's value: 0, 0.5, 1, 1.5, 2, 3, 4, 6, and negative from 8 on.
 __device__ __forceinline__ float e2m1(uint32_t c)
 {
     const uint32_t ex = (c >> 1) & 3, man = c & 1;
@@ -73,27 +84,46 @@ __device__ __forceinline__ float e2m1(uint32_t c)
     return (c & 8) ? -mag : mag;
 }
 
-__global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t *__restrict__ codes,
-                                                         const uint8_t *__restrict__ scales,
-                                                         int64_t nvec, u32x4 *__restrict__ out)
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint32_t *__restrict__ codes,
+                                                              const uint8_t *__restrict__ scales,
+                                                              int64_t nvec, u32x4 *__restrict__ out)
 {
-    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < nvec; i += stride) {
-        const uint32_t c = codes[i];
-        const float s = e8m0(scales[i >> 2]);
-        u32x4 o;
+    const int64_t base = (int64_t)blockIdx.x * kThreads * kUnroll + threadIdx.x;
+    uint32_t cs[kUnroll], bs[kUnroll];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = f32_to_bf16(e2m1(c >> (8 * q)) * s) | (f32_to_bf16(e2m1(c >> (8 * q + 4)) * s) << 16);
-        out[i] = o;
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t i = base + u * kThreads;
+        cs[u] = i < nvec ? codes[i] : 0u;
+        bs[u] = i < nvec ? scales[i >> 2] : 127u;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t i = base + u * kThreads;
+        if (i >= nvec)
+            return;
+        const uint32_t c = cs[u], b = bs[u];
+        u32x4 o;
+        if (b >= 8 && b < 253) {
+            // the packed hardware conversion, where no result is subnormal
+            // or infinite
+            const float s = __uint_as_float(b << 23);
+            o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+            o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+            o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+            o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+        } else {
+            const float s = e8m0(b);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = f32_to_bf16(e2m1(c >> (8 * q)) * s) | (f32_to_bf16(e2m1(c >> (8 * q + 4)) * s) << 16);
+        }
+        __builtin_nontemporal_store(o, out + i);
     }
 }
 
-inline dim3 flat_grid(int64_t nvec)
-{
-    const int64_t want = (nvec + 255) / 256;
-    return dim3((unsigned)(want < 16384 ? want : 16384));
-}
+// Pieces a launch can take: grid x up to 2^31 - 1 workgroups, and fewer than
+// 2^32 threads (2^24 workgroups of 256).
+constexpr int64_t kMostPieces = ((int64_t)1 << 24) * kThreads * kUnroll - kThreads * kUnroll;
 
 }  // namespace
 
@@ -101,8 +131,11 @@ hipError_t launch_mxfp4_quantize(const void *x, int64_t num_rows, int32_t inner,
                                  uint8_t *scales, hipStream_t stream)
 {
     const int64_t nvec = num_rows * (inner / 8);
-    launch(quantize_kernel, flat_grid(nvec), dim3(256), 0, stream, (const u32x4 *)x, nvec,
-           (uint32_t *)codes, scales);
+    for (int64_t at = 0; at < nvec; at += kMostPieces) {
+        const int64_t n = nvec - at < kMostPieces ? nvec - at : kMostPieces;
+        launch(quantize_kernel, dim3((unsigned)((n + kThreads * kUnroll - 1) / (kThreads * kUnroll))), dim3(kThreads),
+               0, stream, (const u32x4 *)x + at, n, (uint32_t *)codes + at, scales + at / 4);
+    }
     return hipGetLastError();
 }
 
@@ -110,8 +143,11 @@ hipError_t launch_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
                                    int32_t inner, void *out, hipStream_t stream)
 {
     const int64_t nvec = num_rows * (inner / 8);
-    launch(dequantize_kernel, flat_grid(nvec), dim3(256), 0, stream, (const uint32_t *)codes,
-           scales, nvec, (u32x4 *)out);
+    for (int64_t at = 0; at < nvec; at += kMostPieces) {
+        const int64_t n = nvec - at < kMostPieces ? nvec - at : kMostPieces;
+        launch(dequantize_kernel, dim3((unsigned)((n + kThreads * kUnroll - 1) / (kThreads * kUnroll))),
+               dim3(kThreads), 0, stream, (const uint32_t *)codes + at, scales + at / 4, n, (u32x4 *)out + at);
+    }
     return hipGetLastError();
 }
 
