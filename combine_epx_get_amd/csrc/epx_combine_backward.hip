@@ -5,7 +5,9 @@
 // (a gather like combine's). One pass does both: a workgroup holds a token's
 // dout chunk in registers, writes the scaled rows and accumulates up to
 // kRows dot products while the y rows stream by. Reads T*h*2 + T*k*h*2 bytes
-// and writes T*k*h*2: HBM bound.
+// and writes T*k*h*2: HBM bound (4096 tokens of 7168, top-8: 196 to 200 us, 5.0
+// to 5.1 TB/s, the rate of a large copy on this card; more chunks in flight a
+// lane measured the same there and 28 us at 384 tokens).
 //
 // A dot product is summed in a fixed order that depends on the launch shape
 // only: ascending chunks in each lane, lanes by xor, waves ascending.
@@ -112,10 +114,11 @@ hipError_t launch_combine_backward(const Geometry &g, const epx_layout &L, const
 {
     const int nvec = hidden / 8;
     // rows per workgroup: all of a token's, but fewer where that leaves less
-    // than about 2048 workgroups
+    // than 512 workgroups (384 tokens of 7168, top-8: 21.6 us, against 24.0 and
+    // 24.8 with 1024 and 2048)
     int per = g.k;
-    if (g.T < 2048) {
-        const int parts = (2048 + g.T - 1) / g.T;
+    if (g.T < 512) {
+        const int parts = (512 + g.T - 1) / g.T;
         per = (g.k + parts - 1) / parts;
     }
     int threads = (nvec + kWave - 1) / kWave * kWave;
