@@ -78,6 +78,9 @@ __device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4 buf, uint32_t o
 // be overwritten.
 template <int PENDING> __device__ __forceinline__ void wait_copies()
 {
+    // the same wait for LDS reads where the compiler counts it (lgkmcnt 0, the
+    // other counters at their most): else it waits for them again later
+    __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
 }
 
