@@ -420,44 +420,65 @@ def epx_plan_swaps(num_experts: int, num_ranks: int, num_hosts: int, expert_coun
 _LOGITS = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _route_args(problem, logits, topk_idx, name, other):
-    shape = (problem.num_tokens, problem.topk)
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
-        raise ValueError("logits: bfloat16 or float32")
-    _need(logits, logits.dtype, "logits", 2)
-    if tuple(logits.shape) != (problem.num_tokens, problem.num_experts):
-        raise ValueError("logits: need [T, E]")
-    _need(topk_idx, torch.int32, "topk_idx", 2)
-    _need(other, torch.float32, name, 2)
-    if tuple(topk_idx.shape) != shape or tuple(other.shape) != shape:
-        raise ValueError(f"topk_idx, {name}: need [T, k]")
+def _device(t, name: str) -> int:
+    """The index of the current device, which the tensors of a call have to be
+    on: the calls launch there, and pointers of another one would be read across."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: need a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+    return dev
+
+
+def _ptr(t, dtype, name: str, shape: tuple, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on the device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, dtype, name, len(shape))
+    if t.shape != shape:
+        raise ValueError(f"{name}: need shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+
+
+def _launch_stream(stream, dev: int) -> int:
+    if stream is None and _raw_current_stream is not None:
+        return _raw_current_stream(dev)
+    return _stream(stream)
+
+
+def _logits_dtype(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _LOGITS:
+        raise ValueError(f"{name}: bfloat16 or float32")
+    return _LOGITS[t.dtype]
 
 
 def epx_route(problem: epx_problem, logits: torch.Tensor, score: int, topk_idx: torch.Tensor,
               topk_weights: torch.Tensor, bias: Optional[torch.Tensor] = None, renormalize: bool = True,
               scale: float = 1.0, stream=None) -> None:
     """Router: the k experts of every token and their weights, from logits [T, E]."""
-    _route_args(problem, logits, topk_idx, "topk_weights", topk_weights)
-    if bias is not None:
-        _need(bias, torch.float32, "bias", 1)
-        if bias.numel() != problem.num_experts:
-            raise ValueError("bias: need [E]")
-    _check(_lib.epx_route(ctypes.byref(problem), logits.data_ptr(), _LOGITS[logits.dtype], score,
-                          bias.data_ptr() if bias is not None else None, int(bool(renormalize)), scale,
-                          topk_idx.data_ptr(), topk_weights.data_ptr(), _stream(stream)), "epx_route")
+    code, dev = _logits_dtype(logits, "logits"), _device(logits, "logits")
+    T, E, k = problem.num_tokens, problem.num_experts, problem.topk
+    _check(_lib.epx_route(ctypes.byref(problem), _ptr(logits, logits.dtype, "logits", (T, E), dev), code, score,
+                          _ptr(bias, torch.float32, "bias", (E,), dev) if bias is not None else None,
+                          int(bool(renormalize)), scale, _ptr(topk_idx, torch.int32, "topk_idx", (T, k), dev),
+                          _ptr(topk_weights, torch.float32, "topk_weights", (T, k), dev),
+                          _launch_stream(stream, dev)), "epx_route")
 
 
 def epx_route_backward(problem: epx_problem, logits: torch.Tensor, score: int, topk_idx: torch.Tensor,
                        dweights: torch.Tensor, dlogits: torch.Tensor, renormalize: bool = True,
                        scale: float = 1.0, stream=None) -> None:
     """Gradient of epx_route's weights: dlogits [T, E] from dweights [T, k]."""
-    _route_args(problem, logits, topk_idx, "dweights", dweights)
-    _need(dlogits, logits.dtype, "dlogits", 2)
-    if dlogits.shape != logits.shape:
-        raise ValueError("dlogits: need [T, E]")
-    _check(_lib.epx_route_backward(ctypes.byref(problem), logits.data_ptr(), _LOGITS[logits.dtype], score,
-                                   int(bool(renormalize)), scale, topk_idx.data_ptr(), dweights.data_ptr(),
-                                   dlogits.data_ptr(), _stream(stream)), "epx_route_backward")
+    code, dev = _logits_dtype(logits, "logits"), _device(logits, "logits")
+    T, E, k = problem.num_tokens, problem.num_experts, problem.topk
+    _check(_lib.epx_route_backward(ctypes.byref(problem), _ptr(logits, logits.dtype, "logits", (T, E), dev), code,
+                                   score, int(bool(renormalize)), scale,
+                                   _ptr(topk_idx, torch.int32, "topk_idx", (T, k), dev),
+                                   _ptr(dweights, torch.float32, "dweights", (T, k), dev),
+                                   _ptr(dlogits, logits.dtype, "dlogits", (T, E), dev),
+                                   _launch_stream(stream, dev)), "epx_route_backward")
 
 
 def epx_combine_backward(problem: epx_problem, layout: Layout, dout: torch.Tensor, y: Optional[torch.Tensor],
@@ -465,25 +486,18 @@ def epx_combine_backward(problem: epx_problem, layout: Layout, dout: torch.Tenso
                          dweights: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradient of epx_combine: dy (rows of y) and, if given, dweights [T, k]
     (without it y is not read and may be None)."""
-    _need(dout, torch.bfloat16, "dout", 2)
-    _need(topk_weights, torch.float32, "topk_weights", 2)
+    dev = _device(dy, "dy")
     _need(dy, torch.bfloat16, "dy", 2)
-    shape = (problem.num_tokens, problem.topk)
-    if tuple(topk_weights.shape) != shape:
-        raise ValueError("topk_weights: need [T, k]")
-    if dout.shape[0] != problem.num_tokens or dout.shape[1] != dy.shape[1]:
-        raise ValueError("dout: need [T, hidden]")
-    if dweights is not None:
-        _need(dweights, torch.float32, "dweights", 2)
-        _need(y, torch.bfloat16, "y", 2)
-        if tuple(dweights.shape) != shape:
-            raise ValueError("dweights: need [T, k]")
-        if y.shape != dy.shape:
-            raise ValueError("y: need the shape of dy")
-    _check(_lib.epx_combine_backward(ctypes.byref(problem), ctypes.byref(layout.struct), dout.data_ptr(),
-                                     y.data_ptr() if dweights is not None else None, dy.shape[0],
-                                     topk_weights.data_ptr(), dout.shape[1], dy.data_ptr(),
-                                     dweights.data_ptr() if dweights is not None else None, _stream(stream)),
+    T, k = problem.num_tokens, problem.topk
+    y_rows, hidden = dy.shape
+    _check(_lib.epx_combine_backward(ctypes.byref(problem), ctypes.byref(layout.struct),
+                                     _ptr(dout, torch.bfloat16, "dout", (T, hidden), dev),
+                                     _ptr(y, torch.bfloat16, "y", (y_rows, hidden), dev)
+                                     if dweights is not None else None, y_rows,
+                                     _ptr(topk_weights, torch.float32, "topk_weights", (T, k), dev), hidden,
+                                     dy.data_ptr(),
+                                     _ptr(dweights, torch.float32, "dweights", (T, k), dev)
+                                     if dweights is not None else None, _launch_stream(stream, dev)),
            "epx_combine_backward")
 
 
@@ -493,8 +507,8 @@ class ExpertRows:
     def __init__(self, row_offset: torch.Tensor, row_count: torch.Tensor, num_rows: int):
         _need(row_offset, torch.int32, "row_offset", 1)
         _need(row_count, torch.int32, "row_count", 1)
-        if row_offset.numel() < row_count.numel():
-            raise ValueError("row_offset: need an entry for every expert of row_count")
+        if row_offset.numel() < row_count.numel() or row_offset.device != row_count.device:
+            raise ValueError("row_offset: need an entry for every expert of row_count, on its device")
         if not 0 <= num_rows < 1 << 31:
             raise ValueError("num_rows: need 0 <= num_rows < 2^31")
         self.row_offset, self.row_count = row_offset, row_count
@@ -509,90 +523,80 @@ def expert_rows(row_offset: torch.Tensor, row_count: torch.Tensor, num_rows: int
     return ExpertRows(row_offset, row_count, num_rows)
 
 
-def _shape(t, dtype, name, *shape):
-    _need(t, dtype, name, len(shape))
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: need shape {list(shape)}, got {list(t.shape)}")
-
-
 def epx_expert_gemm(rows: ExpertRows, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, act: int = ACT_NONE,
                     preact: Optional[torch.Tensor] = None, stream=None) -> None:
     """out[r] = act(x[r] @ w[e].T) for the rows r of every expert e. With
     ACT_SWIGLU w is [n, 2 * width, inner] (gate rows, then up rows) and preact,
     if given, receives the product before the activation."""
-    _need(out, torch.bfloat16, "out", 2)
-    _need(x, torch.bfloat16, "x", 2)
+    dev, bf16 = _device(rows.row_count, "rows"), torch.bfloat16
+    _need(out, bf16, "out", 2)
+    _need(x, bf16, "x", 2)
     width, inner, R = out.shape[1], x.shape[1], rows.num_rows
     wide = 2 * width if act == ACT_SWIGLU else width
-    _shape(x, torch.bfloat16, "x", R, inner)
-    _shape(out, torch.bfloat16, "out", R, width)
-    _shape(w, torch.bfloat16, "w", rows.num_experts, wide, inner)
-    if preact is not None:
-        _shape(preact, torch.bfloat16, "preact", R, wide)
-    _check(_lib.epx_expert_gemm(ctypes.byref(rows.struct), x.data_ptr(), w.data_ptr(), width, inner, act,
-                                preact.data_ptr() if preact is not None else None, out.data_ptr(),
-                                _stream(stream)), "epx_expert_gemm")
+    _check(_lib.epx_expert_gemm(ctypes.byref(rows.struct), _ptr(x, bf16, "x", (R, inner), dev),
+                                _ptr(w, bf16, "w", (rows.num_experts, wide, inner), dev), width, inner, act,
+                                _ptr(preact, bf16, "preact", (R, wide), dev) if preact is not None else None,
+                                _ptr(out, bf16, "out", (R, width), dev), _launch_stream(stream, dev)),
+           "epx_expert_gemm")
 
 
 def epx_expert_gemm_dgrad(rows: ExpertRows, dy: torch.Tensor, w: torch.Tensor, dx: torch.Tensor,
                           input_act: int = ACT_NONE, preact: Optional[torch.Tensor] = None, stream=None) -> None:
     """dx[r] = dy[r] @ w[e]; with input_act=ACT_SWIGLU (the product's input was
     the gated activation of preact) dx is the gradient of preact."""
-    _need(w, torch.bfloat16, "w", 3)
-    width, inner, R = w.shape[1], w.shape[2], rows.num_rows
+    dev, bf16 = _device(rows.row_count, "rows"), torch.bfloat16
+    _need(w, bf16, "w", 3)
+    n, width, inner = w.shape
+    R = rows.num_rows
     wide = 2 * inner if input_act == ACT_SWIGLU else inner
-    _shape(w, torch.bfloat16, "w", rows.num_experts, width, inner)
-    _shape(dy, torch.bfloat16, "dy", R, width)
-    _shape(dx, torch.bfloat16, "dx", R, wide)
-    if preact is not None:
-        _shape(preact, torch.bfloat16, "preact", R, wide)
-    _check(_lib.epx_expert_gemm_dgrad(ctypes.byref(rows.struct), dy.data_ptr(), w.data_ptr(), width, inner,
-                                      input_act, preact.data_ptr() if preact is not None else None,
-                                      dx.data_ptr(), _stream(stream)), "epx_expert_gemm_dgrad")
+    _check(_lib.epx_expert_gemm_dgrad(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev),
+                                      _ptr(w, bf16, "w", (rows.num_experts, width, inner), dev), width, inner,
+                                      input_act,
+                                      _ptr(preact, bf16, "preact", (R, wide), dev) if preact is not None else None,
+                                      _ptr(dx, bf16, "dx", (R, wide), dev), _launch_stream(stream, dev)),
+           "epx_expert_gemm_dgrad")
 
 
 def epx_expert_gemm_wgrad(rows: ExpertRows, dy: torch.Tensor, x: torch.Tensor, dw: torch.Tensor,
                           accumulate: bool = False, stream=None) -> None:
     """dw[e] = dy[r].T @ x[r] summed over the rows of every expert e; bfloat16
     or float32, the latter also added to what dw holds."""
-    if not isinstance(dw, torch.Tensor) or dw.dtype not in _LOGITS:
-        raise ValueError("dw: bfloat16 or float32")
+    code, dev, bf16 = _logits_dtype(dw, "dw"), _device(rows.row_count, "rows"), torch.bfloat16
     _need(dw, dw.dtype, "dw", 3)
-    width, inner, R = dw.shape[1], dw.shape[2], rows.num_rows
-    _shape(dw, dw.dtype, "dw", rows.num_experts, width, inner)
-    _shape(dy, torch.bfloat16, "dy", R, width)
-    _shape(x, torch.bfloat16, "x", R, inner)
-    _check(_lib.epx_expert_gemm_wgrad(ctypes.byref(rows.struct), dy.data_ptr(), x.data_ptr(), width, inner,
-                                      _LOGITS[dw.dtype], int(bool(accumulate)), dw.data_ptr(),
-                                      _stream(stream)), "epx_expert_gemm_wgrad")
+    n, width, inner = dw.shape
+    R = rows.num_rows
+    _check(_lib.epx_expert_gemm_wgrad(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev),
+                                      _ptr(x, bf16, "x", (R, inner), dev), width, inner, code,
+                                      int(bool(accumulate)),
+                                      _ptr(dw, dw.dtype, "dw", (rows.num_experts, width, inner), dev),
+                                      _launch_stream(stream, dev)), "epx_expert_gemm_wgrad")
 
 
 def _mxfp4_args(values, codes, scales, name):
-    """Rows are the product of all dimensions but the last."""
+    """(rows, inner, addresses, device); rows are the product of all dimensions but the last."""
+    dev = _device(values, name)
     _need(values, torch.bfloat16, name)
-    _need(codes, torch.uint8, "codes")
-    _need(scales, torch.uint8, "scales")
     if values.dim() < 2:
         raise ValueError(f"{name}: need at least 2 dimensions")
-    inner = values.shape[-1]
-    lead = tuple(values.shape[:-1])
-    if inner % 32 or tuple(codes.shape) != lead + (inner // 2,) or tuple(scales.shape) != lead + (inner // 32,):
-        raise ValueError("codes, scales: need [..., inner/2] and [..., inner/32], inner a multiple of 32")
-    return values.numel() // inner if inner else 0, inner
+    inner, lead = values.shape[-1], tuple(values.shape[:-1])
+    if inner == 0 or inner % 32:
+        raise ValueError(f"{name}: the last dimension must be a multiple of 32")
+    return (values.numel() // inner, inner, values.data_ptr(),
+            _ptr(codes, torch.uint8, "codes", lead + (inner // 2,), dev),
+            _ptr(scales, torch.uint8, "scales", lead + (inner // 32,), dev), dev)
 
 
 def epx_mxfp4_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """bf16 rows [..., inner] to 4-bit codes [..., inner/2] and scale bytes [..., inner/32]."""
-    num_rows, inner = _mxfp4_args(x, codes, scales, "x")
-    _check(_lib.epx_mxfp4_quantize(x.data_ptr(), num_rows, inner, codes.data_ptr(), scales.data_ptr(),
-                                   _stream(stream)), "epx_mxfp4_quantize")
+    num_rows, inner, px, pc, ps, dev = _mxfp4_args(x, codes, scales, "x")
+    _check(_lib.epx_mxfp4_quantize(px, num_rows, inner, pc, ps, _launch_stream(stream, dev)), "epx_mxfp4_quantize")
 
 
 def epx_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """The bf16 values that 4-bit codes and scale bytes stand for."""
-    num_rows, inner = _mxfp4_args(out, codes, scales, "out")
-    _check(_lib.epx_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), num_rows, inner, out.data_ptr(),
-                                     _stream(stream)), "epx_mxfp4_dequantize")
+    num_rows, inner, po, pc, ps, dev = _mxfp4_args(out, codes, scales, "out")
+    _check(_lib.epx_mxfp4_dequantize(pc, ps, num_rows, inner, po, _launch_stream(stream, dev)),
+           "epx_mxfp4_dequantize")
 
 
 def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
@@ -601,24 +605,21 @@ def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Ten
     """epx_expert_gemm for fp8 rows (codes and a float32 scale per 128 channels,
     as epx_dispatch writes them) and 4-bit weights. out is bfloat16, or uint8
     codes with out_scales [rows, width/128]."""
-    fp8 = isinstance(out, torch.Tensor) and out.dtype == torch.uint8
-    _need(out, torch.uint8 if fp8 else torch.bfloat16, "out", 2)
-    _need(x, torch.uint8, "x", 2)
+    dev, u8, f32 = _device(rows.row_count, "rows"), torch.uint8, torch.float32
+    fp8 = isinstance(out, torch.Tensor) and out.dtype == u8
+    _need(out, u8 if fp8 else torch.bfloat16, "out", 2)
+    _need(x, u8, "x", 2)
+    if out_scales is not None and not fp8:
+        raise ValueError("out_scales: only with uint8 rows out")
     width, inner, R, n = out.shape[1], x.shape[1], rows.num_rows, rows.num_experts
     wide = 2 * width if act == ACT_SWIGLU else width
-    _shape(x, torch.uint8, "x", R, inner)
-    _shape(x_scales, torch.float32, "x_scales", R, inner // 128)
-    _shape(w, torch.uint8, "w", n, wide, inner // 2)
-    _shape(w_scales, torch.uint8, "w_scales", n, wide, inner // 32)
-    _shape(out, out.dtype, "out", R, width)
-    if fp8:
-        _shape(out_scales, torch.float32, "out_scales", R, width // 128)
-    elif out_scales is not None:
-        raise ValueError("out_scales: only with uint8 rows out")
-    _check(_lib.epx_expert_gemm_mxfp4(ctypes.byref(rows.struct), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(),
-                                      w_scales.data_ptr(), width, inner, act, FP8_E4M3 if fp8 else BF16,
-                                      out.data_ptr(), out_scales.data_ptr() if fp8 else None,
-                                      _stream(stream)), "epx_expert_gemm_mxfp4")
+    _check(_lib.epx_expert_gemm_mxfp4(ctypes.byref(rows.struct), _ptr(x, u8, "x", (R, inner), dev),
+                                      _ptr(x_scales, f32, "x_scales", (R, inner // 128), dev),
+                                      _ptr(w, u8, "w", (n, wide, inner // 2), dev),
+                                      _ptr(w_scales, u8, "w_scales", (n, wide, inner // 32), dev), width, inner, act,
+                                      FP8_E4M3 if fp8 else BF16, _ptr(out, out.dtype, "out", (R, width), dev),
+                                      _ptr(out_scales, f32, "out_scales", (R, width // 128), dev) if fp8 else None,
+                                      _launch_stream(stream, dev)), "epx_expert_gemm_mxfp4")
 
 
 def relay_capacity(problem: epx_problem) -> int:
