@@ -50,6 +50,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
     static constexpr int kLds = S * kBuf;
     static constexpr int kLag = 3;
+    static constexpr bool kAtOnce = SUBS * NI * NJ <= 16;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!GLU || NI % 2 == 0, "gate and up fragments pair up in a wave");
     static_assert(!FP8OUT || PC % 128 == 0, "a tile holds whole scale blocks");
@@ -176,60 +177,107 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
             aim(step + S - 1);
             // copies are spread over the step's instructions where there are
             // enough of them; small tiles, which wait for memory, make them first
-            constexpr int kSpread = SUBS * NI * NJ >= 2 * kCopies ? SUBS * NI * NJ / kCopies : 0;
+            constexpr int kSpread = !kAtOnce && SUBS * NI * NJ >= 2 * kCopies ? SUBS * NI * NJ / kCopies : 0;
             if (kSpread == 0) {
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c)
                     copy(c, to);
             }
             const uint32_t at = lds + (uint32_t)buf * kBuf;
+            if constexpr (kAtOnce) {
+                // few instructions a step: everything is read before the first
+                i32x8 pf[SUBS][NI], qf[SUBS][NJ];
+                int sp[SUBS][NI];
+                float sq[SUBS][NJ];
 #pragma unroll
-            for (int s = 0; s < SUBS; ++s) {
-                const uint32_t ps = at + kPBytes + kQBytes + s * (kPScale + kQScale) * 256, qs = ps + kPScale * 256;
-                i32x8 pf[NI], qf[2];
-                int sp[NI];
-                float sq[2];
-                auto read_q = [&](int j) {
-                    const int r = wq * (TQ / WQ) + j * 16 + m;
-                    const uint32_t row = at + kPBytes + r * kQRow;
-                    const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
-                    const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
-                    qf[j & 1] = i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    sq[j & 1] = lds_read<float>(qs + r * 4);
-                };
-                read_q(0);
+                for (int s = 0; s < SUBS; ++s) {
+                    const uint32_t ps = at + kPBytes + kQBytes + s * (kPScale + kQScale) * 256, qs = ps + kPScale * 256;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int r = p_row(wp, i, m);
-                    const i32x4 v = lds_read<i32x4>(at + r * kPRow + (((s * 4 + g) ^ p_key(r)) * 16));
-                    pf[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-                    sp[i] = lds_read<uint8_t>(ps + r * 4 + g);
+                    for (int i = 0; i < NI; ++i) {
+                        const int r = p_row(wp, i, m);
+                        const i32x4 v = lds_read<i32x4>(at + r * kPRow + (((s * 4 + g) ^ p_key(r)) * 16));
+                        pf[s][i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+                        sp[s][i] = lds_read<uint8_t>(ps + r * 4 + g);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const int r = wq * (TQ / WQ) + j * 16 + m;
+                        const uint32_t row = at + kPBytes + r * kQRow;
+                        const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
+                        const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
+                        qf[s][j] = i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        sq[s][j] = lds_read<float>(qs + r * 4);
+                    }
                 }
-                // A block's product is scaled and added three instructions
-                // after its own, which covers its latency.
-                f32x4 d[kLag + 1];
-                float ds[kLag + 1];
+                f32x4 d[SUBS][NI][NJ];
 #pragma unroll
-                for (int x = 0; x < NI * NJ + kLag; ++x) {
-                    const int i = x % NI, j = x / NI;
-                    if (x < NI * NJ) {
-                        const int at_x = s * NI * NJ + x;
-                        if (kSpread > 0 && at_x % (kSpread ? kSpread : 1) == 0 && at_x / (kSpread ? kSpread : 1) < kCopies)
-                            copy(at_x / (kSpread ? kSpread : 1), to);
-                        if (i == 0 && j + 1 < NJ)
-                            read_q(j + 1);
-                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                        d[x % (kLag + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf[j & 1], zero, 4, 0,
-                                                                                            0, sp[i], 0, 127);
-                        ds[x % (kLag + 1)] = sq[j & 1];
-                    }
-                    if (x >= kLag) {
-                        const int y = x - kLag, yi = y % NI, yj = y / NI, k = y % (kLag + 1);
+                for (int s = 0; s < SUBS; ++s)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[yi][yj][q] = __builtin_fmaf(d[k][q], ds[k], acc[yi][yj][q]);
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                            d[s][i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[s][i], qf[s][j], zero, 4, 0, 0,
+                                                                                         sp[s][i], 0, 127);
+                        }
+#pragma unroll
+                for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                acc[i][j][q] = __builtin_fmaf(d[s][i][j][q], sq[s][j], acc[i][j][q]);
+            } else {
+#pragma unroll
+                for (int s = 0; s < SUBS; ++s) {
+                    const uint32_t ps = at + kPBytes + kQBytes + s * (kPScale + kQScale) * 256, qs = ps + kPScale * 256;
+                    i32x8 pf[NI], qf[2];
+                    int sp[NI];
+                    float sq[2];
+                    auto read_q = [&](int j) {
+                        const int r = wq * (TQ / WQ) + j * 16 + m;
+                        const uint32_t row = at + kPBytes + r * kQRow;
+                        const i32x4 lo = lds_read<i32x4>(row + (((s * 8 + g) ^ q_key(r)) * 16));
+                        const i32x4 hi = lds_read<i32x4>(row + (((s * 8 + 4 + g) ^ q_key(r)) * 16));
+                        qf[j & 1] = i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        sq[j & 1] = lds_read<float>(qs + r * 4);
+                    };
+                    read_q(0);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int r = p_row(wp, i, m);
+                        const i32x4 v = lds_read<i32x4>(at + r * kPRow + (((s * 4 + g) ^ p_key(r)) * 16));
+                        pf[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+                        sp[i] = lds_read<uint8_t>(ps + r * 4 + g);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    // A block's product is scaled and added three instructions
+                    // after its own, which covers its latency.
+                    f32x4 d[kLag + 1];
+                    float ds[kLag + 1];
+#pragma unroll
+                    for (int x = 0; x < NI * NJ + kLag; ++x) {
+                        const int i = x % NI, j = x / NI;
+                        if (x < NI * NJ) {
+                            const int at_x = s * NI * NJ + x;
+                            if (kSpread > 0 && at_x % (kSpread ? kSpread : 1) == 0 && at_x / (kSpread ? kSpread : 1) < kCopies)
+                                copy(at_x / (kSpread ? kSpread : 1), to);
+                            if (i == 0 && j + 1 < NJ)
+                                read_q(j + 1);
+                            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                            d[x % (kLag + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[i], qf[j & 1], zero, 4, 0,
+                                                                                                0, sp[i], 0, 127);
+                            ds[x % (kLag + 1)] = sq[j & 1];
+                        }
+                        if (x >= kLag) {
+                            const int y = x - kLag, yi = y % NI, yj = y / NI, k = y % (kLag + 1);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                acc[yi][yj][q] = __builtin_fmaf(d[k][q], ds[k], acc[yi][yj][q]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
             buf = buf + 1 == S ? 0 : buf + 1;
