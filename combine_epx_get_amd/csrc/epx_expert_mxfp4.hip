@@ -50,7 +50,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
     static constexpr int kLds = S * kBuf;
     static constexpr int kLag = 3;
-    static constexpr bool kAtOnce = SUBS * NI * NJ <= 16;
+    static constexpr bool kAtOnce = WQ == 1 && SUBS * NI * NJ <= 16;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!GLU || NI % 2 == 0, "gate and up fragments pair up in a wave");
     static_assert(!FP8OUT || PC % 128 == 0, "a tile holds whole scale blocks");
