@@ -75,7 +75,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
         else
             return (r & 3) | (((r >> H) & 1) << 2);
     }
-    static __device__ __forceinline__ int q_key(int r) { return (r & 3) | (((r >> 2) & 1) << 2); }
+    static __device__ __forceinline__ int q_key(int r) { return r & (8 * SUBS - 1); }
 
     static __device__ __forceinline__ void run(const Args &a, const Tile &t, char *smem)
     {
