@@ -15,6 +15,12 @@
 // 16) on; Q, the 16 codes from 16 * (lane / 16) on and the 16 from 64 + 16 *
 // (lane / 16) on. Tiles, copies, ring of buffers and chunk permutation as in
 // the bf16 products; the scales come to LDS beside the codes.
+//
+// Few rows an expert: a CU's rate of reading bounds it (64 rows over 8 experts
+// of 2 x 2048 x 7168: 28.7 us, of which about 8 do not depend on the size).
+// Many: the matrix cores, whose clock falls to 1.5 GHz under these
+// instructions (32768 ragged rows, 16 experts of 2 x 2048 x 7168: 888-922 us,
+// 2.1 PFLOP/s; a library product of E4M3 with E4M3 reached 2.7 at 8192^3).
 #include "epx_gemm.h"
 
 namespace epx {
