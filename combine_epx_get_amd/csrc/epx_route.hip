@@ -13,9 +13,10 @@
 // or absent place and key 1 a masked expert (-infinity or NaN); every other
 // key is larger.
 //
-// Bound by instruction issue from a few thousand tokens on (16384 tokens, 256
-// experts, top-8, float32: 9.8 us, 1.7 TB/s; the gradient about as long, 3.4
-// TB/s), by launch latency below (128 tokens: 6.9 us a call).
+// Bound by a call's own time, about 6.5 us, up to some thousand tokens (128
+// tokens of 256 experts, biased: 6.9 us); 16384 tokens of 256 experts, top-8,
+// float32, take 9.4 us, the gradient 7.9 (17 and 34 MB). A biased choice is
+// bound by its double precision exponentials there (21 us).
 #include "epx_device.h"
 
 namespace epx {
@@ -36,26 +37,80 @@ __device__ __forceinline__ uint64_t sortable(double f)
     return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// All lanes of a token (L of them, L / 16 rows) combined by `op`, the same
+// bits in every lane: rotations within a row, then swaps of rows (no LDS).
+template <int N> __device__ __forceinline__ uint32_t row_ror(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-        v += __shfl_xor(v, d, kWave);
+    return (uint32_t)dpp<kDppRowRor + N>((int)v);
+}
+template <int N> __device__ __forceinline__ float row_ror(float v)
+{
+    return __uint_as_float(row_ror<N>(__float_as_uint(v)));
+}
+template <int N> __device__ __forceinline__ double row_ror(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double(
+        (long long)(((uint64_t)row_ror<N>((uint32_t)(b >> 32)) << 32) | row_ror<N>((uint32_t)b)));
+}
+// The other row of a pair of rows (N = 16) or half of the wave (N = 32): the
+// pair (x of the lower, x of the higher) in both.
+template <int N> __device__ __forceinline__ void both(uint32_t v, uint32_t &lo, uint32_t &hi)
+{
+    typedef uint32_t u32p __attribute__((ext_vector_type(2)));
+    u32p p;
+    if constexpr (N == 16)
+        p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    else
+        p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    lo = p.x;
+    hi = p.y;
+}
+template <int N> __device__ __forceinline__ void both(float v, float &lo, float &hi)
+{
+    uint32_t a, b;
+    both<N>(__float_as_uint(v), a, b);
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+template <int N> __device__ __forceinline__ void both(double v, double &lo, double &hi)
+{
+    const uint64_t bits = (uint64_t)__double_as_longlong(v);
+    uint32_t a, b, c, d;
+    both<N>((uint32_t)(bits >> 32), a, b);
+    both<N>((uint32_t)bits, c, d);
+    lo = __longlong_as_double((long long)(((uint64_t)a << 32) | c));
+    hi = __longlong_as_double((long long)(((uint64_t)b << 32) | d));
+}
+template <int L, typename T, typename F> __device__ __forceinline__ T over_token(T v, F op)
+{
+    v = op(v, row_ror<8>(v));
+    v = op(v, row_ror<4>(v));
+    v = op(v, row_ror<2>(v));
+    v = op(v, row_ror<1>(v));
+    if constexpr (L >= 32) {
+        T lo, hi;
+        both<16>(v, lo, hi);
+        v = op(lo, hi);
+    }
+    if constexpr (L == 64) {
+        T lo, hi;
+        both<32>(v, lo, hi);
+        v = op(lo, hi);
+    }
     return v;
 }
-__device__ __forceinline__ float wave_maxf(float v)
+template <int L> __device__ __forceinline__ uint32_t token_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor(v, d, kWave));
-    return v;
+    return over_token<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-__device__ __forceinline__ double wave_sum(double v)
+template <int L> __device__ __forceinline__ float token_maxf(float v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-        v += __shfl_xor(v, d, kWave);
-    return v;
+    return over_token<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L, typename T> __device__ __forceinline__ T token_sum(T v)
+{
+    return over_token<L>(v, [](T a, T b) { return a + b; });
 }
 
 __device__ __forceinline__ bool masked(float l) { return !(l > -__builtin_inff()); }
@@ -101,37 +156,6 @@ __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-
 __device__ __forceinline__ float exp_to(float l, float m)
 {
     return masked(l) ? 0.0f : l == m ? 1.0f : expf(l - m);
-}
-
-// Maximum over the L lanes of a token.
-template <int L> __device__ __forceinline__ uint32_t token_max(uint32_t v)
-{
-    v = max(v, (uint32_t)dpp<kDppRowShr + 1>((int)v));
-    v = max(v, (uint32_t)dpp<kDppRowShr + 2>((int)v));
-    v = max(v, (uint32_t)dpp<kDppRowShr + 4>((int)v));
-    v = max(v, (uint32_t)dpp<kDppRowShr + 8>((int)v));
-    v = max(v, (uint32_t)dpp<kDppRowBcast15, 0xa, false>((int)v));
-    if (L == 32) {
-        const int low = __builtin_amdgcn_readlane((int)v, 31), high = __builtin_amdgcn_readlane((int)v, 63);
-        return (uint32_t)(lane_id() < 32 ? low : high);
-    }
-    v = max(v, (uint32_t)dpp<kDppRowBcast31, 0xc, false>((int)v));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
-}
-
-template <int L, typename T> __device__ __forceinline__ T token_sum(T v)
-{
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1)
-        v += __shfl_xor(v, d, L);
-    return v;
-}
-template <int L> __device__ __forceinline__ float token_maxf(float v)
-{
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor(v, d, L));
-    return v;
 }
 
 template <typename TIn, int PER, int L, bool BIASED>
@@ -189,6 +213,7 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn *__restrict__ logi
             }
     }
 
+    const uint64_t below = (1ull << lane) - 1;   // the token's lower lanes
     for (int j = 0; j < k; ++j) {
         uint32_t bh = hi[0], bl = BIASED ? lo[0] : 0u;
         int bi = 0;
@@ -208,12 +233,8 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn *__restrict__ logi
             best = best && bl == wl;
         }
         // the lowest lane of each token
-        uint64_t win = __ballot(best);
-        if (L == 32)
-            win = ((uint32_t)win & -(uint32_t)win) | ((uint64_t)((uint32_t)(win >> 32) & -(uint32_t)(win >> 32)) << 32);
-        else
-            win &= -win;
-        if ((win >> lane_id()) & 1) {
+        const uint64_t all = __ballot(best);
+        if (best && ((L == 64 ? all : all >> (lane_id() & -L)) & below) == 0) {
             if (kSorted) {
                 s_pick[tok][j] = id[0];
 #pragma unroll
@@ -284,17 +305,19 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn *__restrict__ logi
     }
 }
 
-// dlogits of one token; lane j < k holds (id, score, dweight) of choice j.
-template <typename TIn, int PER>
+// dlogits; lane j < k of the L lanes of a token holds (id, score, dweight) of
+// choice j, and every lane the gradients of PER consecutive experts.
+template <typename TIn, int PER, int L>
 __global__ __launch_bounds__(256) void route_backward_kernel(
     const TIn *__restrict__ logits, int64_t T, int E, int k, bool softmax, bool renormalize,
     float scale, const int32_t *__restrict__ idx, const float *__restrict__ dweights,
     TIn *__restrict__ dlogits)
 {
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T)
-        return;
-    const int lane = lane_id(), at = lane * PER;
+    constexpr int kTokens = 256 / L;   // of a workgroup
+    struct Choice { int32_t id; float part; };
+    __shared__ Choice s_choice[kTokens][L];
+    const int tok = threadIdx.x / L, lane = threadIdx.x % L, at = lane * PER;
+    const int64_t t_own = (int64_t)blockIdx.x * kTokens + tok, t = t_own < T ? t_own : T - 1;
     const TIn *row = logits + t * E;
     int e = -1;
     float g = 0.0f, le = -__builtin_inff();
@@ -319,46 +342,49 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             m = fmaxf(m, l[i]);
-        m = wave_maxf(m);
+        m = token_maxf<L>(m);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             sum += exp_to(l[i], m);
-        sum = wave_sum(sum);
+        sum = token_sum<L>(sum);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         const float p = exp_to(le, m) * inv;
         c = e >= 0 ? g * p : 0.0f;
-        const float all = wave_sum(c);
+        const float all = token_sum<L>(c);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             d[i] = -(exp_to(l[i], m) * inv) * all;
     } else if (softmax) {
-        const float m = wave_maxf(le);
+        const float m = token_maxf<L>(le);
         const float x = e >= 0 ? exp_to(le, m) : 0.0f;
-        const float sum = wave_sum(x);
+        const float sum = token_sum<L>(x);
         const float p = sum > 0.0f ? x / sum : 0.0f;
-        const float mean = wave_sum(e >= 0 ? g * p : 0.0f);
+        const float mean = token_sum<L>(e >= 0 ? g * p : 0.0f);
         c = e >= 0 ? p * (g - mean) : 0.0f;
     } else {
         // 1 - p is formed as 1 / (1 + exp(l)): p alone loses it near 1
         const bool on = e >= 0 && !masked(le);
         const double p = on ? sigmoid64(le) : 0.0, q = on ? 1.0 / (1.0 + exp((double)le)) : 0.0;
         if (renormalize) {
-            const double sum = wave_sum(p);
+            const double sum = token_sum<L>(p);
             const double r = sum > 0.0 ? p / sum : 0.0;
-            const double mean = wave_sum(on ? (double)g * r : 0.0);
+            const double mean = token_sum<L>(on ? (double)g * r : 0.0);
             c = on ? (float)(r * ((double)g - mean) * q) : 0.0f;
         } else {
             c = on ? (float)((double)g * p * q) : 0.0f;
         }
     }
+    s_choice[tok][lane] = Choice{e, c};
+    __syncthreads();
     for (int j = 0; j < k; ++j) {   // in order: an id given twice counts twice
-        const int ej = __builtin_amdgcn_readlane(e, j);
-        const float cj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(c), j));
+        const Choice own = s_choice[tok][j];
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (at + i == ej)
-                d[i] += cj;
+            if (at + i == own.id)
+                d[i] += own.part;
     }
+    if (t_own >= T)
+        return;
     TIn *out = dlogits + t * E;
     struct alignas(PER * sizeof(TIn) < 16 ? PER * sizeof(TIn) : 16) Pack { TIn v[PER]; };
     Pack o;
@@ -380,21 +406,39 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
     }
 }
 
-// Places per lane for E experts: the smallest power of two with 64 lanes.
-template <typename F> void with_per(int E, F f)
+// Lanes for a token's gradient, and places per lane, the smallest power of two
+// for E experts with them. Half a wave up to 256 experts where it holds the
+// choices too (16384 tokens of 256 experts, top-8, softmax of the chosen / of
+// all / sigmoid: 7.9 / 11.9 / 8.5 us; 9.6 / 13.2 / 9.8 with 16 lanes; a wave,
+// with sums through LDS, 9.7 / 12.9 / 11.5).
+template <typename F> void with_shape(int E, int k, F f)
 {
-    if (E <= 64)
-        f(std::integral_constant<int, 1>());
-    else if (E <= 128)
-        f(std::integral_constant<int, 2>());
-    else if (E <= 256)
-        f(std::integral_constant<int, 4>());
-    else if (E <= 512)
-        f(std::integral_constant<int, 8>());
-    else if (E <= 1024)
-        f(std::integral_constant<int, 16>());
-    else
-        f(std::integral_constant<int, 32>());
+    const std::integral_constant<int, 64> wave;
+    const std::integral_constant<int, 32> part;
+    if (k > 32 || E > 256) {
+        if (E <= 64)
+            f(std::integral_constant<int, 1>(), wave);
+        else if (E <= 128)
+            f(std::integral_constant<int, 2>(), wave);
+        else if (E <= 256)
+            f(std::integral_constant<int, 4>(), wave);
+        else if (E <= 512)
+            f(std::integral_constant<int, 8>(), wave);
+        else if (E <= 1024)
+            f(std::integral_constant<int, 16>(), wave);
+        else
+            f(std::integral_constant<int, 32>(), wave);
+    } else if (E <= 32) {
+        f(std::integral_constant<int, 1>(), part);
+    } else if (E <= 2 * 32) {
+        f(std::integral_constant<int, 2>(), part);
+    } else if (E <= 4 * 32) {
+        f(std::integral_constant<int, 4>(), part);
+    } else if (E <= 8 * 32) {
+        f(std::integral_constant<int, 8>(), part);
+    } else {
+        f(std::integral_constant<int, 16>(), part);
+    }
 }
 
 }  // namespace
@@ -422,8 +466,9 @@ hipError_t launch_route(const Geometry &g, const void *logits, bool bf16, bool s
             go((float *)nullptr, std::false_type());
     };
     // Half a wave a token up to 256 experts: a round's maximum and ballot then
-    // serve two tokens (16384 tokens, 256 experts, top-8: 9.8 us, against
-    // 13.3 with a wave each).
+    // serve two tokens (16384 tokens, 256 experts, top-8: 9.4 us, against
+    // 13.3 with a wave each; 16 lanes 9.2, but 11.8 against 7.2 for 128 biased
+    // tokens).
     using H = std::integral_constant<int, 32>;
     using W = std::integral_constant<int, 64>;
     if (g.E <= 32)
@@ -447,15 +492,15 @@ hipError_t launch_route_backward(const Geometry &g, const void *logits, bool bf1
                                  bool renormalize, float scale, const int32_t *idx,
                                  const float *dweights, void *dlogits, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((g.T + 3) / 4));
-    with_per(g.E, [&](auto per) {
-        constexpr int P = decltype(per)::value;
+    with_shape(g.E, g.k, [&](auto per, auto lanes) {
+        constexpr int P = decltype(per)::value, L = decltype(lanes)::value;
+        const dim3 grid((unsigned)((g.T + 256 / L - 1) / (256 / L)));
         if (bf16)
-            launch(route_backward_kernel<uint16_t, P>, grid, dim3(256), 0, stream,
+            launch(route_backward_kernel<uint16_t, P, L>, grid, dim3(256), 0, stream,
                    (const uint16_t *)logits, (int64_t)g.T, g.E, g.k, softmax, renormalize, scale,
                    idx, dweights, (uint16_t *)dlogits);
         else
-            launch(route_backward_kernel<float, P>, grid, dim3(256), 0, stream,
+            launch(route_backward_kernel<float, P, L>, grid, dim3(256), 0, stream,
                    (const float *)logits, (int64_t)g.T, g.E, g.k, softmax, renormalize, scale, idx,
                    dweights, (float *)dlogits);
     });
