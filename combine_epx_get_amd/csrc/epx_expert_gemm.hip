@@ -16,6 +16,10 @@
 // bits of the row index, in the copies' source addresses, so that the reads
 // of a fragment touch every LDS bank equally.
 //
+// Few tiles: groups of waves divide a tile's sum among them, each with a ring
+// of its own, and add their sums up through LDS in a fixed order; no memory of
+// a call's own and no second launch is needed.
+//
 // Reads past an operand's last row, column or sum index return zeros (the
 // buffer descriptors' range check), so ragged tiles need no other code; a
 // tile writes the rows and columns that exist.
@@ -48,16 +52,24 @@ struct Args {
 // Rows of BK: the rows of a fragment differ in their low two bits and in bit
 // `high`. Rows of columns: see read_cols.
 template <int HIGH> __device__ __forceinline__ int row_key(int r) { return (r & 3) | (((r >> HIGH) & 1) << 2); }
-__device__ __forceinline__ int col_key(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
+template <int T> __device__ __forceinline__ int col_key(int k)
+{
+    // rows of 64 (32) columns: two (four) of them fill the banks once, so the
+    // row's lowest bits separate them already
+    const int key = (k & 3) | (((k >> 3) & 1) << 2);
+    return T == 32 ? (key & 4) >> 1 : T == 64 ? key & 6 : key << 1;
+}
 
 __host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
 
-template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
+// WP x WQ waves compute a tile; WK groups of them take every WK-th step each,
+// with buffers of their own, and add up their sums at the end.
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> struct Kernel {
     static constexpr bool kGlu = OP == kForwardGlu;
     static constexpr bool kPCols = OP >= kDgrad;     // P's sum index is the row in memory
     static constexpr bool kWeights = OP >= kWgrad;
     static constexpr bool kQCols = kWeights;
-    static constexpr int kWaves = WP * WQ, kThreads = kWaves * kWave;
+    static constexpr int kWaves = WP * WQ;   // of a group
     static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
     // P fragments whose rows are read such that a lane has 4 * GI consecutive
     // columns of them
@@ -66,7 +78,9 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     static constexpr int kPBytes = TP * BK * 2, kQBytes = TQ * BK * 2;
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
     static constexpr bool kDeep = TP == 256;
-    static constexpr int kLds = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
+    static constexpr int kRing = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
+    static constexpr int kLds = WK * kRing;
+    static_assert(WK == 1 || (!kDeep && kRing >= TP * TQ * 4), "a group's sums fit its buffers");
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
 
@@ -92,7 +106,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
             if constexpr (COLS) {
                 constexpr int lanes = T / 8;   // lanes per row of the tile
                 const int k = inst * (64 / lanes) + lane_id() / lanes;
-                const int chunk = (lane_id() % lanes) ^ col_key(k);
+                const int chunk = (lane_id() % lanes) ^ col_key<T>(k);
                 off[c] = (uint32_t)(k * ld + chunk * 8) * 2u;
             } else {
                 constexpr int lanes = BK / 8;
@@ -113,7 +127,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
     {
         const int l = lane_id(), g = l >> 4, j = (l >> 2) & 3;
         const int k = s * 32 + g * 8 + j;
-        const int chunk = (col / 8 + ((l & 3) >> 1)) ^ col_key(k);
+        const int chunk = (col / 8 + ((l & 3) >> 1)) ^ col_key<T>(k);
         const uint32_t at = buf + k * (T * 2) + chunk * 16 + (l & 1) * 8;
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
         const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 4 * T * 2));
@@ -129,8 +143,8 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
 
     static __device__ __forceinline__ void run(const Args &a, const Tile &t, char *smem)
     {
-        const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
-        const int m = lane_id() & 15, g = lane_id() >> 4;
+        const int of_all = uniform(threadIdx.x >> 6), group = of_all / kWaves;
+        const int wave = of_all % kWaves, wp = wave % WP, wq = wave / WP, m = lane_id() & 15;
         constexpr int PK = 2 + log2i(GI), QK = 2;   // row_key bits
 
         const int sum = kWeights ? t.sum : a.sum;
@@ -160,12 +174,12 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         uint32_t p_off[kPCopies], q_off[kQCopies];
         copy_offsets<kPCols, TP, kPCopies, PK, kGlu>(wave, kPCols ? 0 : col0, kPCols ? a.np : sum, a.np, p_off);
         copy_offsets<kQCols, TQ, kQCopies, QK, false>(wave, 0, kQCols ? a.nq : sum, 0, q_off);
-        const uint32_t lds = lds_offset(smem);
+        const uint32_t lds = lds_offset(smem) + (uint32_t)group * kRing;
 
-        // descriptors of the operands' parts in a step (empty past the last)
+        // descriptors of the operands' parts in a group's step (empty past the last)
         i32x4 rp, rq;
-        auto aim = [&](int step) {
-            const int k0 = step * BK;
+        auto aim = [&](int own) {
+            const int step = own * WK + group, k0 = step * BK;
             const bool live = step < steps;
             if constexpr (kPCols)
                 rp = buffer_of(pb + (int64_t)k0 * a.np * 2,
@@ -314,8 +328,12 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
             for (int s = 0; s < S - 1; ++s)
                 issue(s, s);
             int buf = 0;
-            for (int step = 0; step < steps; ++step) {
-                wait_copies<(S - 2) * (kPCopies + kQCopies)>();
+            const int own_steps = (steps + WK - 1) / WK;
+            for (int step = 0; step < own_steps; ++step) {
+                if constexpr (WK > 1 && kWaves == 1)
+                    wait_own_copies<(S - 2) * (kPCopies + kQCopies)>();
+                else
+                    wait_copies<(S - 2) * (kPCopies + kQCopies)>();
                 int into = buf + S - 1;
                 into = into >= S ? into - S : into;
                 issue(step + S - 1, into);
@@ -340,23 +358,64 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
         }
         drain_copies();
 
-        // Results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
-        // columns 4 g .. 4 g + 3 of fragment i. Two fragments are neighbours
-        // already where P's rows are read that way (GI), and are merged here
-        // otherwise, so that the lanes of a write are neighbours in 64 bytes
-        // of a row (float32 results are so as they are).
+        if constexpr (WK == 1) {
+            write<NJ>(a, t, wp, wq, 0, acc);
+        } else {
+            // Every group's sums go to LDS; each of them then adds up the sums
+            // of some columns of fragments, in the order of the groups.
+            constexpr int NE = (NJ + WK - 1) / WK;
+            static_assert(NJ % NE == 0, "");
+            if constexpr (kWaves > 1)
+                __syncthreads();   // the group's waves are done with its buffers
+            auto at = [&](int of, int i, int j) {
+                return lds_offset(smem) + (uint32_t)of * kRing + (uint32_t)((((wave * NI + i) * NJ + j) * kWave + lane_id()) * 16);
+            };
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    *(__attribute__((address_space(3))) f32x4 *)(uintptr_t)at(group, i, j) = acc[i][j];
+            __syncthreads();
+            const int j0 = group * NE;
+            if (j0 >= NJ)
+                return;
+            f32x4 all[NI][NE];
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    all[i][j] = lds_read<f32x4>(at(0, i, j0 + j));
+#pragma unroll
+                    for (int of = 1; of < WK; ++of)
+                        all[i][j] += lds_read<f32x4>(at(of, i, j0 + j));
+                }
+            write<NE>(a, t, wp, wq, j0, all);
+        }
+    }
+
+    // Results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
+    // columns 4 g .. 4 g + 3 of fragment i. Two fragments are neighbours
+    // already where P's rows are read that way (GI), and are merged here
+    // otherwise, so that the lanes of a write are neighbours in 64 bytes
+    // of a row (float32 results are so as they are).
+    template <int N>
+    static __device__ __forceinline__ void write(const Args &a, const Tile &t, int wp, int wq, int j0, f32x4 (&acc)[NI][N])
+    {
+        const int m = lane_id() & 15, g = lane_id() >> 4;
+        constexpr int PC = kGlu ? TP / 2 : TP;
+        const int col0 = t.p * PC;
         constexpr bool kMerge = kPCols && OP != kWgradF32 && NI % 2 == 0;
         constexpr int W = kMerge ? 2 : GI, NG = kHalf / W;
         if constexpr (kMerge) {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
                     merge_columns(acc[2 * n][j], acc[2 * n + 1][j]);
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int r = wq * (TQ / WQ) + j * 16 + m;
+        for (int j = 0; j < N; ++j) {
+            const int r = wq * (TQ / WQ) + (j0 + j) * 16 + m;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const int c = col0 + wp * (PC / WP) + n * 16 * W + 4 * W * g;
@@ -413,10 +472,10 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ> struct Kernel {
 };
 
 // The large tiles' kernels carry the smaller ones for an expert's last rows.
-template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
-__global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK>
+__global__ __launch_bounds__(WP *WQ *WK *kWave) void gemm_kernel(Args a)
 {
-    using K = Kernel<OP, TP, TQ, BK, S, WP, WQ>;
+    using K = Kernel<OP, TP, TQ, BK, S, WP, WQ, WK>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
     Tile t;
     if constexpr (K::kWeights) {
@@ -447,7 +506,7 @@ __global__ __launch_bounds__(WP *WQ *kWave) void gemm_kernel(Args a)
     }
 }
 
-template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ>
+template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1>
 hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
 {
     constexpr int PC = OP == kForwardGlu ? TP / 2 : TP;
@@ -461,11 +520,39 @@ hipError_t start(Args a, int64_t rows_or_n, hipStream_t stream)
     }
     if (blocks == 0)
         return hipSuccess;
-    if (blocks * WP * WQ * kWave > (int64_t)0xFFFFFFFF)
+    constexpr int kThreads = WP * WQ * WK * kWave;
+    if (blocks * kThreads > (int64_t)0xFFFFFFFF)
         return hipErrorInvalidConfiguration;
-    launch(gemm_kernel<OP, TP, TQ, BK, S, WP, WQ>, dim3((unsigned)blocks), dim3(WP * WQ * kWave), 0,
+    launch(gemm_kernel<OP, TP, TQ, BK, S, WP, WQ, WK>, dim3((unsigned)blocks), dim3(kThreads), 0,
            stream, a);
     return hipGetLastError();
+}
+
+// Where small tiles would leave CUs idle: the largest tile of which there are
+// at most 256, one workgroup a CU whose waves divide the sum among them. False
+// when there are more of every size. FULL: a tile of 32's columns.
+// Measured, us, 32 x 32 / 64 x 32 / 64 x 64 / the tiles that are taken else
+// (forward; with how many tiles there are of each): 3 experts of 1 row, gated
+// 560 x 3712 (105, 54, 54) 9.4 / 12.7 / 15.5 / 19.3; 1 of 64 rows, gated
+// 2048 x 7168 (256, 128, 64) 15.8 / 20.1 / 24.7 / 33.3; 1 of 699 rows, 544 x
+// 1016 (374, 198, 99) 10.6 / 8.4 / 8.8 / 9.7; 4 of 256 rows, 1024 x 2048
+// (1024, 512, 256) 24.8 / 18.1 / 11.7 / 15.2; 3 of 1000 rows, 512 x 2048 (1536,
+// 768, 384) 35.2 / 25.6 / 20.4 / 19.5. Gradient of the input: 1 of 8 rows, 2048
+// x 7168 (224, 112, 112) 8.9 / 10.1 / 11.3 / 16.2; 16 of 64 rows, 512 x 1024
+// (1024, 512, 256) 19.2 / 11.3 / 8.2 / 8.6.
+template <int OP>
+bool start_split(const Args &a, int64_t rows, hipStream_t stream, hipError_t &status)
+{
+    constexpr int FULL = OP == kForwardGlu ? 16 : 32;
+    if (tiles_of(a.r, 32, a.np, FULL) <= 256)
+        status = start<OP, 32, 32, 64, 2, 1, 1, 8>(a, rows, stream);
+    else if (tiles_of(a.r, 32, a.np, 2 * FULL) <= 256)
+        status = start<OP, 64, 32, 64, 3, 1, 1, 4>(a, rows, stream);
+    else if (tiles_of(a.r, 64, a.np, 2 * FULL) <= 256)
+        status = start<OP, 64, 64, 64, 2, 1, 1, 4>(a, rows, stream);
+    else
+        return false;
+    return true;
 }
 
 }  // namespace
@@ -494,6 +581,9 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
     //   rows 17.1 / 11.1 / 11.8, 384 rows 28.6 / 21.6 / 29.7;
     //   8 of 2048 x 7168, 256 ragged rows: 106 / 82 / 113.
     const int64_t rows = r.num_rows, n = r.n;
+    hipError_t status;
+    if (swiglu ? start_split<kForwardGlu>(a, rows, stream, status) : start_split<kForward>(a, rows, stream, status))
+        return status;
     if (rows > 64 * n && tiles_of(r, 256, width, swiglu ? 128 : 256) >= 256)
         return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, rows, stream)
                       : start<kForward, 256, 256, 64, 2, 4, 2>(a, rows, stream);
@@ -519,6 +609,10 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     // each 84.5 / 87.1, 256 rows 131 / 198; 64 of 1024 x 2048, 16 rows 44.8 /
     // 43.1, 96 rows 56 / 74; 16 of 512 x 1024 (64 to 128 large tiles), 256 rows
     // 21.0 / 10.7, 384 rows 22.3 / 17.3.
+    hipError_t status;
+    if (preact ? start_split<kDgradGlu>(a, r.num_rows, stream, status)
+               : start_split<kDgrad>(a, r.num_rows, stream, status))
+        return status;
     if (tiles_of(r, 256, inner, 256) >= 256)
         return preact ? start<kDgradGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
@@ -544,8 +638,25 @@ hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *
     // (bf16), 213 / 185 (float32), 256 rows 263 / 243, 294 / 330, 1024 rows
     // 519 / 569, 545 / 703; 64 of 1024 x 2048, 64 rows 105 / 85, 1024 rows
     // 308 / 345; 8 of 512 x 1024 (64 large tiles), 1024 rows 31 / 20.
-    const int64_t tiles = (int64_t)((width + 255) / 256) * ((inner + 255) / 256) * r.n;
-    if (tiles >= 128 && r.num_rows >= 384 * (int64_t)r.n)
+    // Few tiles (a workgroup a CU at most): half as large ones, whose waves
+    // divide the sum among them, else four pairs of waves on a tile; the same
+    // for two rounds of workgroups if the sums are long. Against the small
+    // tiles: 2 experts of 376 x 648, 5200 rows each (132 tiles of 64 x 64) 29 /
+    // 68 (pairs 34), 4 of 512 x 512, 512 rows (256 tiles) 7.0 / 11.9 (8.0); 4 of
+    // 512 x 1024 (256 tiles of 128 x 64), 256 rows 7.8 / 9.2, 4096 rows 27.6 /
+    // 56.5 (64 x 64: 36); 8 of 512 x 1024, 1024 rows 21.3 / 20.8, 4096 rows 48.5
+    // / 57.2; 5 of 320 x 1432 (300), 800 rows 19.5 / 16.7, 3000 rows 40.4 / 42.1.
+    const auto tiles_of_size = [&](int w, int i) {
+        return (int64_t)((width + w - 1) / w) * ((inner + i - 1) / i) * r.n;
+    };
+    const int64_t mid = tiles_of_size(64, 128);
+    if (tiles_of_size(64, 64) <= 256)
+        return f32 ? start<kWgradF32, 64, 64, 64, 2, 1, 1, 4>(a, r.n, stream)
+                   : start<kWgrad, 64, 64, 64, 2, 1, 1, 4>(a, r.n, stream);
+    if (mid <= 256 || (mid <= 512 && r.num_rows >= 1024 * (int64_t)r.n))
+        return f32 ? start<kWgradF32, 128, 64, 32, 3, 2, 1, 4>(a, r.n, stream)
+                   : start<kWgrad, 128, 64, 32, 3, 2, 1, 4>(a, r.n, stream);
+    if (tiles_of_size(256, 256) >= 128 && r.num_rows >= 384 * (int64_t)r.n)
         return f32 ? start<kWgradF32, 256, 256, 64, 2, 4, 2>(a, r.n, stream)
                    : start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
     return f32 ? start<kWgradF32, 128, 128, 32, 3, 2, 2>(a, r.n, stream)

@@ -84,6 +84,13 @@ template <int PENDING> __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
 }
 
+// The same for buffers that only this wave uses.
+template <int PENDING> __device__ __forceinline__ void wait_own_copies()
+{
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PENDING) : "memory");
+}
+
 // Every copy of this wave is done (before its LDS is given back).
 __device__ __forceinline__ void drain_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 

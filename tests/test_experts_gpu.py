@@ -66,6 +66,11 @@ CASES = [
     ("150 experts, every kind of last tile", [(i * 53) % 300 for i in range(150)], 1, None, 264, 520),
     ("very wide", [700, 300], 0, [1, 0], 16392, 136),
     ("very long sum", [700, 300], 2, None, 136, 16392),
+    ("few tiles, a sum that ends inside a group's step", [33, 0, 64, 7], 1, None, 264, 2104),
+    ("64 experts", [(i * 53) % 128 for i in range(64)], 0, None, 520, 328),
+    ("middle, wide", [40, 0, 64, 65, 90, 31, 2, 130], 0, None, 2056, 2056),
+    ("five experts, wide", [100, 0, 60, 200, 64], 0, None, 1032, 1032),
+    ("few experts, many rows", [2100, 0, 1900], 0, None, 520, 2056),
 ]
 IDS = [c[0] for c in CASES]
 
