@@ -555,6 +555,14 @@ bool start_split(const Args &a, int64_t rows, hipStream_t stream, hipError_t &st
     return true;
 }
 
+// Large tiles that occupy the GPU, and whether square ones of 128 rows do
+// (measured at the callers).
+constexpr int64_t kEnoughLarge = 200;
+bool square_tiles(const ExpertRows &r, int32_t columns, int tile_columns)
+{
+    return r.num_rows >= 160 * (int64_t)r.n && tiles_of(r, 128, columns, tile_columns) > 288;
+}
+
 }  // namespace
 
 hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w, int32_t width,
@@ -580,13 +588,23 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
     //   16 of 512 x 1024 (64 to 128 large tiles), 16 rows 12.1 / 9.5 / 8.3, 128
     //   rows 17.1 / 11.1 / 11.8, 384 rows 28.6 / 21.6 / 29.7;
     //   8 of 2048 x 7168, 256 ragged rows: 106 / 82 / 113.
+    // From 160 rows an expert, where large tiles are too few, square ones (two
+    // workgroups a CU) if they are more than a round of workgroups; large /
+    // square / 64 rows: 11 of 466 rows, 1960 x 472 (200 large tiles, 720 square)
+    // 22.9 / 28.2 / 30.3; 4 of 2600 rows, 656 x 1120 (126, 504) 33.8 / 27.9 /
+    // 36.3; 6 of 700 rows, gated 704 x 1200 (114, 385) 32.6 / 24.8 / 29.7; 8 of
+    // 512 rows, 1024 x 512 (80, 288) 19.7 / 12.5 / 10.7; 16 of 96 rows, 2048 x
+    // 1024 (128, 320) 19.4 / 20.1 / 17.0.
     const int64_t rows = r.num_rows, n = r.n;
     hipError_t status;
     if (swiglu ? start_split<kForwardGlu>(a, rows, stream, status) : start_split<kForward>(a, rows, stream, status))
         return status;
-    if (rows > 64 * n && tiles_of(r, 256, width, swiglu ? 128 : 256) >= 256)
+    if (rows > 64 * n && tiles_of(r, 256, width, swiglu ? 128 : 256) >= kEnoughLarge)
         return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, rows, stream)
                       : start<kForward, 256, 256, 64, 2, 4, 2>(a, rows, stream);
+    if (square_tiles(r, width, swiglu ? 64 : 128))
+        return swiglu ? start<kForwardGlu, 128, 128, 64, 2, 2, 2>(a, rows, stream)
+                      : start<kForward, 128, 128, 64, 2, 2, 2>(a, rows, stream);
     if (rows > 20 * n && tiles_of(r, 64, width, swiglu ? 64 : 128) >= 256)
         return swiglu ? start<kForwardGlu, 128, 64, 64, 3, 4, 1>(a, rows, stream)
                       : start<kForward, 128, 64, 64, 3, 4, 1>(a, rows, stream);
@@ -608,14 +626,20 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     // Measured, us, large / small tiles: 16 experts of 2048 x 7168, 16 rows
     // each 84.5 / 87.1, 256 rows 131 / 198; 64 of 1024 x 2048, 16 rows 44.8 /
     // 43.1, 96 rows 56 / 74; 16 of 512 x 1024 (64 to 128 large tiles), 256 rows
-    // 21.0 / 10.7, 384 rows 22.3 / 17.3.
+    // 21.0 / 10.7, 384 rows 22.3 / 17.3. Large / square / small: 4 of 2600 rows,
+    // 656 x 1120 (210 large tiles, 738 square) 28.6 / 33.5 / 35.4; 8 of 1500
+    // rows, 1432 x 320 (100, 291) 37.8 / 28.3 / 30.5; 6 of 700 rows, 1200 x 704
+    // (57, 210) 33.0 / 21.1 / 18.6.
     hipError_t status;
     if (preact ? start_split<kDgradGlu>(a, r.num_rows, stream, status)
                : start_split<kDgrad>(a, r.num_rows, stream, status))
         return status;
-    if (tiles_of(r, 256, inner, 256) >= 256)
+    if (tiles_of(r, 256, inner, 256) >= kEnoughLarge)
         return preact ? start<kDgradGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
+    if (square_tiles(r, inner, 128))
+        return preact ? start<kDgradGlu, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream)
+                      : start<kDgrad, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream);
     return preact ? start<kDgradGlu, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream)
                   : start<kDgrad, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream);
 }

@@ -71,6 +71,7 @@ CASES = [
     ("middle, wide", [40, 0, 64, 65, 90, 31, 2, 130], 0, None, 2056, 2056),
     ("five experts, wide", [100, 0, 60, 200, 64], 0, None, 1032, 1032),
     ("few experts, many rows", [2100, 0, 1900], 0, None, 520, 2056),
+    ("square tiles, odd sizes", [1500, 0, 901, 303], 1, None, 1800, 1672),
 ]
 IDS = [c[0] for c in CASES]
 
