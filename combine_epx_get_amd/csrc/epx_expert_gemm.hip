@@ -80,7 +80,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
     static constexpr bool kDeep = TP == 256;
     static constexpr int kRing = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
     static constexpr int kLds = WK * kRing;
-    static_assert(WK == 1 || (!kDeep && kRing >= TP * TQ * 4), "a group's sums fit its buffers");
+    static_assert(WK == 1 || !kDeep, "");
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
 
@@ -361,35 +361,11 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
         if constexpr (WK == 1) {
             write<NJ>(a, t, wp, wq, 0, acc);
         } else {
-            // Every group's sums go to LDS; each of them then adds up the sums
-            // of some columns of fragments, in the order of the groups.
             constexpr int NE = (NJ + WK - 1) / WK;
-            static_assert(NJ % NE == 0, "");
-            if constexpr (kWaves > 1)
-                __syncthreads();   // the group's waves are done with its buffers
-            auto at = [&](int of, int i, int j) {
-                return lds_offset(smem) + (uint32_t)of * kRing + (uint32_t)((((wave * NI + i) * NJ + j) * kWave + lane_id()) * 16);
-            };
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    *(__attribute__((address_space(3))) f32x4 *)(uintptr_t)at(group, i, j) = acc[i][j];
-            __syncthreads();
-            const int j0 = group * NE;
-            if (j0 >= NJ)
-                return;
             f32x4 all[NI][NE];
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int j = 0; j < NE; ++j) {
-                    all[i][j] = lds_read<f32x4>(at(0, i, j0 + j));
-#pragma unroll
-                    for (int of = 1; of < WK; ++of)
-                        all[i][j] += lds_read<f32x4>(at(of, i, j0 + j));
-                }
-            write<NE>(a, t, wp, wq, j0, all);
+            join_groups<WK, kRing, kWaves>(lds_offset(smem), group, wave, acc, all);
+            if (group * NE < NJ)
+                write<NE>(a, t, wp, wq, group * NE, all);
         }
     }
 

@@ -38,9 +38,11 @@ struct Args {
 
 __host__ __device__ constexpr int log2i(int v) { return v <= 1 ? 0 : 1 + log2i(v / 2); }
 
-// SUBS blocks of 128 channels a step.
-template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ> struct Kernel {
-    static constexpr int kWaves = WP * WQ;
+// SUBS blocks of 128 channels a step. WP x WQ waves compute a tile; WK groups
+// of them take every WK-th step each, with buffers of their own, and add up
+// their sums at the end.
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ, int WK = 1> struct Kernel {
+    static constexpr int kWaves = WP * WQ;   // of a group
     static constexpr int NI = TP / WP / 16, NJ = TQ / WQ / 16;
     static constexpr int kHalf = GLU ? NI / 2 : NI;
     static constexpr int GI = kHalf % 2 == 0 ? 2 : 1;
@@ -50,17 +52,17 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kPCopies = kPBytes / 1024 / kWaves, kQCopies = kQBytes / 1024 / kWaves;
     // scale words: one of 4 bytes per row and block, 64 rows a copy; rounded
     // up so that every wave makes the same number of copies
-    static constexpr int kPScale = TP / 64, kQScale = (TQ + 63) / 64;
+    static constexpr int kPScale = (TP + 63) / 64, kQScale = (TQ + 63) / 64;
     static constexpr int kScales = SUBS * (kPScale + kQScale);
     static constexpr int kSCopies = (kScales + kWaves - 1) / kWaves;
     static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
-    static constexpr int kLds = S * kBuf;
+    static constexpr int kRing = S * kBuf, kLds = WK * kRing;
     static constexpr int kLag = 3;
     static constexpr bool kAtOnce = WQ == 1 && SUBS * NI * NJ <= 16;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!GLU || NI % 2 == 0, "gate and up fragments pair up in a wave");
     static_assert(!FP8OUT || PC % 128 == 0, "a tile holds whole scale blocks");
-    static_assert(TP % 64 == 0 && SUBS <= 2, "");
+    static_assert(SUBS <= 2, "");
 
     static __device__ __forceinline__ int p_row(int wp, int i, int m)
     {
@@ -85,7 +87,8 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
 
     static __device__ __forceinline__ void run(const Args &a, const Tile &t, char *smem)
     {
-        const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
+        const int of_all = uniform(threadIdx.x >> 6), group = of_all / kWaves;
+        const int wave = of_all % kWaves, wp = wave % WP, wq = wave / WP;
         const int lane = lane_id(), m = lane & 15, g = lane >> 4;
         const int blocks = a.sum / 128, steps = (blocks + SUBS - 1) / SUBS;
         const int col0 = t.p * PC;
@@ -122,12 +125,13 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
             const bool in = inst < kScales && (is_p ? r < TP : r < TQ);
             s_off[c] = in ? (uint32_t)(is_p ? weight_row(r) : r) * sld + (uint32_t)sub * 4u : kOutside;
         }
-        const uint32_t lds = lds_offset(smem);
+        const uint32_t lds = lds_offset(smem) + (uint32_t)group * kRing;
 
-        // descriptors of the operands' parts in a step (empty past the last)
+        // descriptors of the operands' parts in a group's step (empty past the last)
         i32x4 rp, rq, rps, rqs;
         int left = 0;   // blocks from the step's first to the sum's end
-        auto aim = [&](int step) {
+        auto aim = [&](int own) {
+            const int step = own * WK + group;
             const bool live = step < steps;
             const int b0 = step * SUBS;   // first block of 128
             rp = buffer_of(pb + (int64_t)b0 * 64, live ? p_bytes - (uint32_t)b0 * 64u : 0u);
@@ -175,8 +179,12 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
                 copy(c, lds + (uint32_t)s * kBuf);
         }
         int buf = 0;
-        for (int step = 0; step < steps; ++step) {
-            wait_copies<(S - 2) * kCopies>();
+        const int own_steps = (steps + WK - 1) / WK;
+        for (int step = 0; step < own_steps; ++step) {
+            if constexpr (WK > 1 && kWaves == 1)
+                wait_own_copies<(S - 2) * kCopies>();
+            else
+                wait_copies<(S - 2) * kCopies>();
             int into = buf + S - 1;
             into = into >= S ? into - S : into;
             const uint32_t to = lds + (uint32_t)into * kBuf;
@@ -290,6 +298,23 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
         }
         drain_copies();
 
+        if constexpr (WK == 1) {
+            write<NJ>(a, t, wp, wq, 0, acc, smem);
+        } else {
+            constexpr int NE = (NJ + WK - 1) / WK;
+            f32x4 all[NI][NE];
+            join_groups<WK, kRing, kWaves>(lds_offset(smem), group, wave, acc, all);
+            static_assert(!FP8OUT || WK * NE == NJ, "every wave meets the others there");
+            if (group * NE < NJ)
+                write<NE>(a, t, wp, wq, group * NE, all, smem);
+        }
+    }
+
+    template <int N>
+    static __device__ __forceinline__ void write(const Args &a, const Tile &t, int wp, int wq, int j0,
+                                                 f32x4 (&acc)[NI][N], char *smem)
+    {
+        const int m = lane_id() & 15, g = lane_id() >> 4, col0 = t.p * PC;
         constexpr int NG = kHalf / GI;
         if constexpr (FP8OUT) {
             // activation in place, then the largest magnitude of every row in
@@ -300,7 +325,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
             float *s_max = (float *)smem;   // [WP][TQ]
             __syncthreads();                // every wave is done with the operands
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
+            for (int j = 0; j < N; ++j) {
                 float mx = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i)
@@ -313,12 +338,12 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
                 mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
                 mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
                 if (g == 0)
-                    s_max[wp * TQ + wq * (TQ / WQ) + j * 16 + m] = mx;
+                    s_max[wp * TQ + wq * (TQ / WQ) + (j0 + j) * 16 + m] = mx;
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int r = wq * (TQ / WQ) + j * 16 + m;
+            for (int j = 0; j < N; ++j) {
+                const int r = wq * (TQ / WQ) + (j0 + j) * 16 + m;
                 if (r >= t.rows)
                     continue;
                 const int64_t row = t.row0 + r;
@@ -346,8 +371,8 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int r = wq * (TQ / WQ) + j * 16 + m;
+            for (int j = 0; j < N; ++j) {
+                const int r = wq * (TQ / WQ) + (j0 + j) * 16 + m;
                 if (r >= t.rows)
                     continue;
                 uint16_t *out = (uint16_t *)a.out + (int64_t)(t.row0 + r) * a.np;
@@ -369,10 +394,10 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     }
 };
 
-template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ>
-__global__ __launch_bounds__(WP *WQ *kWave) void mx_kernel(Args a)
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ, int WK>
+__global__ __launch_bounds__(WP *WQ *WK *kWave) void mx_kernel(Args a)
 {
-    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>;
+    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ, WK>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
     constexpr bool kSplit = TQ == 256;   // the large tiles carry smaller ones for an expert's last rows
     Tile t;
@@ -390,18 +415,18 @@ __global__ __launch_bounds__(WP *WQ *kWave) void mx_kernel(Args a)
     }
 }
 
-template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ>
+template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ, int WK = 1>
 hipError_t start(Args a, hipStream_t stream)
 {
-    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>;
+    using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ, WK>;
+    constexpr int kThreads = WP * WQ * WK * kWave;
     a.pt = (a.np + K::PC - 1) / K::PC;
     const int64_t blocks = tile_blocks(most_row_tiles(a.r.num_rows, a.r.n, TQ) * a.pt);
     if (blocks == 0)
         return hipSuccess;
-    if (blocks * WP * WQ * kWave > (int64_t)0xFFFFFFFF)
+    if (blocks * kThreads > (int64_t)0xFFFFFFFF)
         return hipErrorInvalidConfiguration;
-    launch(mx_kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ>, dim3((unsigned)blocks), dim3(WP * WQ * kWave), 0,
-           stream, a);
+    launch(mx_kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ, WK>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -414,6 +439,30 @@ template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stre
     // tiles), 64 rows 9.8 / 8.9 / 9.0, 192 rows 19.2 / 11.1 / 12.7, 384 rows
     // 20.2 / 17.0 / 21.9.
     const int64_t rows = a.r.num_rows, n = a.r.n;
+    // Where small tiles would leave CUs idle: the largest tile of which there
+    // are at most 256, one workgroup a CU whose waves divide the sum among
+    // them. Measured, us, 32 x 32 / 64 x 32 / 64 x 64 / the tiles that are taken
+    // else (with how many tiles there are of each): 1 expert of 64 rows, gated
+    // 2048 x 7168 (256, 128, 64) 10.1 / 12.4 / 15.9 / 21.2; 4 of 16 rows (512,
+    // 256, 256) 19.5 / 17.0 / 18.1 / 21.4; 8 of 8 rows (1024, 512, 512) 34 / 30
+    // / 33 / 22.8; 2 of 1187 rows, 256 x 3200 (600, 300, 152) 18.3 / 15.5 / 11.3
+    // / 16.7; 5 of 827 rows, 320 x 1408 (1310, 655, 330) 26.6 / 16.7 / 14.1 /
+    // 10.2. fp8 rows out, whose scale blocks need 128 columns a tile: 4 of 256
+    // rows, 512 x 2048 (136 tiles) 8.7 / 13.1; 1 of 1 row, gated 2048 x 7168
+    // (16) 26.6 / 34.1, but 8 of 8 rows (128) 38.4 / 35.9.
+    if constexpr (FP8OUT) {
+        const int64_t tiles = tiles_of(a.r, 32, a.np, 128);
+        if (tiles <= 32 || (tiles <= 256 && rows > 28 * n))
+            return start<GLU, FP8OUT, GLU ? 256 : 128, 32, 1, 3, 4, 1, 2>(a, stream);
+    } else {
+        constexpr int kFull = GLU ? 16 : 32;   // columns of a tile of 32
+        if (tiles_of(a.r, 32, a.np, kFull) <= 256)
+            return start<GLU, FP8OUT, 32, 32, 1, 3, 1, 1, 8>(a, stream);
+        if (tiles_of(a.r, 32, a.np, 2 * kFull) <= 256)
+            return start<GLU, FP8OUT, 64, 32, 1, 3, 1, 1, 6>(a, stream);
+        if (tiles_of(a.r, 64, a.np, 2 * kFull) <= 256)
+            return start<GLU, FP8OUT, 64, 64, 1, 3, 1, 1, 4>(a, stream);
+    }
     if (rows > 28 * n && tiles_of(a.r, 256, a.np, GLU ? 128 : 256) >= 256)
         return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 4>(a, stream);
     // fp8 rows out need whole scale blocks of 128 columns in a tile

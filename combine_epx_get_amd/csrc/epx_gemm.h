@@ -113,6 +113,40 @@ __device__ __forceinline__ void mfma_in_place(f32x4 &c, bf16x8 a, bf16x8 b)
 // result of a 16x16 instruction can need.
 __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+// Sums of WK groups of waves that divided a tile's sum: every group's go to its
+// RING bytes of LDS, and each of them adds up, in the order of the groups, NE
+// of the NJ columns of fragments, from j0 = group * NE on (groups past the
+// last get none). WAVES waves a group; the groups' copies have arrived.
+template <int WK, int RING, int WAVES, int NI, int NJ, int NE>
+__device__ __forceinline__ void join_groups(uint32_t lds, int group, int wave, const f32x4 (&acc)[NI][NJ],
+                                            f32x4 (&all)[NI][NE])
+{
+    static_assert(NJ % NE == 0 && WK * NE >= NJ && RING >= WAVES * NI * NJ * kWave * 16, "");
+    auto at = [&](int of, int i, int j) {
+        return lds + (uint32_t)of * RING + (uint32_t)((((wave * NI + i) * NJ + j) * kWave + lane_id()) * 16);
+    };
+    if constexpr (WAVES > 1)
+        __syncthreads();   // a group's waves are done with its buffers
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            *(__attribute__((address_space(3))) f32x4 *)(uintptr_t)at(group, i, j) = acc[i][j];
+    __syncthreads();
+    const int j0 = group * NE;
+    if (j0 >= NJ)
+        return;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            all[i][j] = lds_read<f32x4>(at(0, i, j0 + j));
+#pragma unroll
+            for (int of = 1; of < WK; ++of)
+                all[i][j] += lds_read<f32x4>(at(of, i, j0 + j));
+        }
+}
+
 // ---------------------------------------------------------------- tiles
 // Rows of expert e, 0 for a range outside the buffers.
 __device__ __forceinline__ int rows_of(const ExpertRows &r, int e, int &off)

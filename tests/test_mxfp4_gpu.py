@@ -92,7 +92,10 @@ def test_dequantise_every_code_and_scale(epx):
 
 # as for the bf16 products, with inner a multiple of 128 and an inner of one,
 # two and an odd number of blocks
-CASES = [(n, c, gap, o, N, 128 * (1 + (K // 72) % 9)) for n, c, gap, o, N, K in BF16_CASES]
+CASES = [(n, c, gap, o, N, 128 * (1 + (K // 72) % 9)) for n, c, gap, o, N, K in BF16_CASES] + [
+    ("few tiles, 21 blocks", [33, 0, 64, 7], 1, None, 264, 2688),
+    ("some tiles, 29 blocks", [100, 0, 60, 150], 0, None, 520, 3712),
+    ("more tiles, 23 blocks", [290, 2, 260], 2, [2, 0, 1], 808, 2944)]
 
 
 def operands(g, n, M, R, K, epx):
@@ -127,7 +130,10 @@ def test_product(epx, case, act):
 @pytest.mark.parametrize("case", [("one", [1], 0, None, 128, 128), ("decode", [0, 3, 17, 1], 2, None, 384, 640),
                                   ("middle", [50, 0, 90, 64], 1, [2, 0, 1, 3], 256, 384),
                                   ("more rows", [130, 257, 3], 0, None, 640, 256),
-                                  ("large tiles", [(i * 53) % 300 for i in range(150)], 1, None, 384, 256)],
+                                  ("large tiles", [(i * 53) % 300 for i in range(150)], 1, None, 384, 256),
+                                  ("few rows, 60 experts", [i % 5 for i in range(60)], 0, None, 256, 640),
+                                  ("middle, wide", [40, 64, 0, 130, 200, 61, 150, 55], 0, None, 1536, 384),
+                                  ("few tiles, 21 blocks", [70, 3], 1, None, 256, 2688)],
                          ids=lambda c: c[0])
 def test_product_to_fp8_rows(epx, case, act):
     name, cnt, gap, order, N, K = case
