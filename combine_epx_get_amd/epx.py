@@ -168,6 +168,8 @@ class Layout:
 # per call against about 3 us for torch.cuda.current_stream() (measured on
 # MI355X), which is a third of a decode-sized call's host time.
 _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The same for the current device (0.1 us against 0.2), once a CUDA tensor exists.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
@@ -425,7 +427,7 @@ def _device(t, name: str) -> int:
     on: the calls launch there, and pointers of another one would be read across."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: need a CUDA tensor")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if t.get_device() != dev:
         raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
     return dev
@@ -433,13 +435,33 @@ def _device(t, name: str) -> int:
 
 def _ptr(t, dtype, name: str, shape: tuple, dev: int) -> int:
     """Address of a contiguous tensor of this type and shape on the device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:   # no tensor
+        pass
     _need(t, dtype, name, len(shape))
     if t.shape != shape:
         raise ValueError(f"{name}: need shape {list(shape)}, got {list(t.shape)}")
     raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+
+
+def _columns(t, dtype, name: str) -> int:
+    """Columns of a tensor of two dimensions (whose shape _ptr checks)."""
+    try:
+        _, n = t.shape
+    except (AttributeError, ValueError):
+        _need(t, dtype, name, 2)
+        raise ValueError(f"{name}: need 2 dimensions") from None
+    return n
+
+
+def _rows_device(rows) -> int:
+    """As _device, for row ranges (CUDA tensors, checked when they were made)."""
+    dev = _current_device()
+    if rows.device != dev:
+        raise ValueError(f"rows: on device {rows.device}, the current device is {dev}")
+    return dev
 
 
 def _launch_stream(stream, dev: int) -> int:
@@ -512,7 +534,7 @@ class ExpertRows:
         if not 0 <= num_rows < 1 << 31:
             raise ValueError("num_rows: need 0 <= num_rows < 2^31")
         self.row_offset, self.row_count = row_offset, row_count
-        self.num_experts, self.num_rows = row_count.numel(), int(num_rows)
+        self.num_experts, self.num_rows, self.device = row_count.numel(), int(num_rows), row_count.get_device()
         self.struct = epx_expert_rows(self.num_experts, self.num_rows, row_offset.data_ptr(), row_count.data_ptr())
 
 
@@ -528,10 +550,8 @@ def epx_expert_gemm(rows: ExpertRows, x: torch.Tensor, w: torch.Tensor, out: tor
     """out[r] = act(x[r] @ w[e].T) for the rows r of every expert e. With
     ACT_SWIGLU w is [n, 2 * width, inner] (gate rows, then up rows) and preact,
     if given, receives the product before the activation."""
-    dev, bf16 = _device(rows.row_count, "rows"), torch.bfloat16
-    _need(out, bf16, "out", 2)
-    _need(x, bf16, "x", 2)
-    width, inner, R = out.shape[1], x.shape[1], rows.num_rows
+    dev, bf16 = _rows_device(rows), torch.bfloat16
+    width, inner, R = _columns(out, bf16, "out"), _columns(x, bf16, "x"), rows.num_rows
     wide = 2 * width if act == ACT_SWIGLU else width
     _check(_lib.epx_expert_gemm(ctypes.byref(rows.struct), _ptr(x, bf16, "x", (R, inner), dev),
                                 _ptr(w, bf16, "w", (rows.num_experts, wide, inner), dev), width, inner, act,
@@ -544,9 +564,12 @@ def epx_expert_gemm_dgrad(rows: ExpertRows, dy: torch.Tensor, w: torch.Tensor, d
                           input_act: int = ACT_NONE, preact: Optional[torch.Tensor] = None, stream=None) -> None:
     """dx[r] = dy[r] @ w[e]; with input_act=ACT_SWIGLU (the product's input was
     the gated activation of preact) dx is the gradient of preact."""
-    dev, bf16 = _device(rows.row_count, "rows"), torch.bfloat16
-    _need(w, bf16, "w", 3)
-    n, width, inner = w.shape
+    dev, bf16 = _rows_device(rows), torch.bfloat16
+    try:
+        n, width, inner = w.shape
+    except (AttributeError, ValueError):
+        _need(w, bf16, "w", 3)
+        raise ValueError("w: need 3 dimensions") from None
     R = rows.num_rows
     wide = 2 * inner if input_act == ACT_SWIGLU else inner
     _check(_lib.epx_expert_gemm_dgrad(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev),
@@ -561,8 +584,9 @@ def epx_expert_gemm_wgrad(rows: ExpertRows, dy: torch.Tensor, x: torch.Tensor, d
                           accumulate: bool = False, stream=None) -> None:
     """dw[e] = dy[r].T @ x[r] summed over the rows of every expert e; bfloat16
     or float32, the latter also added to what dw holds."""
-    code, dev, bf16 = _logits_dtype(dw, "dw"), _device(rows.row_count, "rows"), torch.bfloat16
-    _need(dw, dw.dtype, "dw", 3)
+    code, dev, bf16 = _logits_dtype(dw, "dw"), _rows_device(rows), torch.bfloat16
+    if dw.dim() != 3:
+        raise ValueError(f"dw: need 3 dimensions, got {tuple(dw.shape)}")
     n, width, inner = dw.shape
     R = rows.num_rows
     _check(_lib.epx_expert_gemm_wgrad(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev),
@@ -605,19 +629,18 @@ def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Ten
     """epx_expert_gemm for fp8 rows (codes and a float32 scale per 128 channels,
     as epx_dispatch writes them) and 4-bit weights. out is bfloat16, or uint8
     codes with out_scales [rows, width/128]."""
-    dev, u8, f32 = _device(rows.row_count, "rows"), torch.uint8, torch.float32
-    fp8 = isinstance(out, torch.Tensor) and out.dtype == u8
-    _need(out, u8 if fp8 else torch.bfloat16, "out", 2)
-    _need(x, u8, "x", 2)
+    dev, u8, f32 = _rows_device(rows), torch.uint8, torch.float32
+    fp8 = isinstance(out, torch.Tensor) and out.dtype is u8
+    rtype = u8 if fp8 else torch.bfloat16
     if out_scales is not None and not fp8:
         raise ValueError("out_scales: only with uint8 rows out")
-    width, inner, R, n = out.shape[1], x.shape[1], rows.num_rows, rows.num_experts
+    width, inner, R, n = _columns(out, rtype, "out"), _columns(x, u8, "x"), rows.num_rows, rows.num_experts
     wide = 2 * width if act == ACT_SWIGLU else width
     _check(_lib.epx_expert_gemm_mxfp4(ctypes.byref(rows.struct), _ptr(x, u8, "x", (R, inner), dev),
                                       _ptr(x_scales, f32, "x_scales", (R, inner // 128), dev),
                                       _ptr(w, u8, "w", (n, wide, inner // 2), dev),
                                       _ptr(w_scales, u8, "w_scales", (n, wide, inner // 32), dev), width, inner, act,
-                                      FP8_E4M3 if fp8 else BF16, _ptr(out, out.dtype, "out", (R, width), dev),
+                                      FP8_E4M3 if fp8 else BF16, _ptr(out, rtype, "out", (R, width), dev),
                                       _ptr(out_scales, f32, "out_scales", (R, width // 128), dev) if fp8 else None,
                                       _launch_stream(stream, dev)), "epx_expert_gemm_mxfp4")
 
