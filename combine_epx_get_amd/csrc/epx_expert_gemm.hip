@@ -531,12 +531,30 @@ bool start_split(const Args &a, int64_t rows, hipStream_t stream, hipError_t &st
     return true;
 }
 
-// Large tiles that occupy the GPU, and whether square ones of 128 rows do
-// (measured at the callers).
-constexpr int64_t kEnoughLarge = 200;
-bool square_tiles(const ExpertRows &r, int32_t columns, int tile_columns)
+// Large tiles (256 x 256, one a CU), square ones (128 x 128, two a CU) or small
+// ones (128 x 64, two a CU): what takes the least time by the number of rounds
+// of workgroups and the time of a round, which is about linear in the length of
+// the sum (16 experts of 2048 rows and 2048 columns, sums of 64 / 256 / 512 /
+// 1024 / 2048: large 47 / 73 / 90 / 130 / 230 us in 4 rounds and the last
+// tiles', square 50 / 69 / 100 / 158 / 321 in 8, small 70 / 90 / 126 / 203 /
+// 394 in 16; a small round is put a quarter higher, for the operands that more
+// tiles read again). Large / square / small elsewhere: 2 experts of 6700 rows,
+// 1080 x 368 36 / 26 / 35; 13 of 917, 1064 x 1536 76 / 55 / 74; 3 of 3189, 1144
+// x 624 26 / 31 / 31; 64 of 96, 1024 x 2048 59 / 61 / 71; 16 of 96, 2048 x 1024
+// 19 / 20 / 17. Gradient of the input: 2 of 11246 rows, 4624 x 368 107 / 144 /
+// 144; 4 of 2600, 656 x 1120 29 / 34 / 35; 8 of 1500, 1432 x 320 38 / 28 / 31;
+// 6 of 700, 1200 x 704 33 / 21 / 19.
+enum TileSize { kLarge, kSquare, kSmall };
+TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, int64_t sum)
 {
-    return r.num_rows >= 160 * (int64_t)r.n && tiles_of(r, 128, columns, tile_columns) > 288;
+    auto rounds = [&](int height, int width, int64_t slots) {
+        return (tiles_of(r, height, columns, columns_of_256 * width / 256) + slots - 1) / slots;
+    };
+    // ns
+    const int64_t large = rounds(256, 256, 256) * (9000 + sum * 47 / 2);
+    const int64_t square = rounds(128, 128, 512) * (4500 + sum * 33 / 2);
+    const int64_t small = rounds(64, 128, 512) * (4200 + sum * 63 / 5);
+    return large <= square && large <= small ? kLarge : square <= small ? kSquare : kSmall;
 }
 
 }  // namespace
@@ -553,35 +571,29 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
     a.sum = inner;
     a.preact_out = (uint16_t *)preact;
     a.out = out;
-    // Large tiles where they occupy the GPU and most experts have more than
-    // the 64 rows of the next size; that one above the 32 rows of the
-    // smallest (a tile more reads an expert's weights again), unless its
-    // tiles leave CUs idle. Measured, us, large / 64 rows / 32 rows, gated:
+    // From 64 rows an expert the sizes of best_tiles. Below, tiles of 64 rows
+    // above the 32 of the smallest (a tile more reads an expert's weights again),
+    // unless they leave CUs idle (of 64 and 32 rows: 7 experts of 2136 rows, 112 x
+    // 7160 59 / 78, 2 of 647, 1408 x 2920 27 / 38). Measured, us, large / 64 rows / 32 rows, gated:
     //   16 experts of 2048 x 7168, 16 rows each 156 / 157 / 157, 48 rows
-    //   159 / 159 / 198, 96 rows 167 / 219 / 283, 256 rows 215 / 403 / 554;
-    //   64 of 1024 x 2048, 16 rows 128 / 113 / 108, 64 rows 132 / 115 / 121,
-    //   128 rows 143 / 138 / 182, 192 rows 164 / 182 / 245;
-    //   16 of 512 x 1024 (64 to 128 large tiles), 16 rows 12.1 / 9.5 / 8.3, 128
-    //   rows 17.1 / 11.1 / 11.8, 384 rows 28.6 / 21.6 / 29.7;
+    //   159 / 159 / 198, 96 rows 167 / 219 / 283;
+    //   64 of 1024 x 2048, 16 rows 128 / 113 / 108, 64 rows 132 / 115 / 121;
+    //   16 of 512 x 1024 (64 to 128 large tiles), 16 rows 12.1 / 9.5 / 8.3;
     //   8 of 2048 x 7168, 256 ragged rows: 106 / 82 / 113.
-    // From 160 rows an expert, where large tiles are too few, square ones (two
-    // workgroups a CU) if they are more than a round of workgroups; large /
-    // square / 64 rows: 11 of 466 rows, 1960 x 472 (200 large tiles, 720 square)
-    // 22.9 / 28.2 / 30.3; 4 of 2600 rows, 656 x 1120 (126, 504) 33.8 / 27.9 /
-    // 36.3; 6 of 700 rows, gated 704 x 1200 (114, 385) 32.6 / 24.8 / 29.7; 8 of
-    // 512 rows, 1024 x 512 (80, 288) 19.7 / 12.5 / 10.7; 16 of 96 rows, 2048 x
-    // 1024 (128, 320) 19.4 / 20.1 / 17.0.
     const int64_t rows = r.num_rows, n = r.n;
     hipError_t status;
     if (swiglu ? start_split<kForwardGlu>(a, rows, stream, status) : start_split<kForward>(a, rows, stream, status))
         return status;
-    if (rows > 64 * n && tiles_of(r, 256, width, swiglu ? 128 : 256) >= kEnoughLarge)
-        return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, rows, stream)
-                      : start<kForward, 256, 256, 64, 2, 4, 2>(a, rows, stream);
-    if (square_tiles(r, width, swiglu ? 64 : 128))
-        return swiglu ? start<kForwardGlu, 128, 128, 64, 2, 2, 2>(a, rows, stream)
-                      : start<kForward, 128, 128, 64, 2, 2, 2>(a, rows, stream);
-    if (rows > 20 * n && tiles_of(r, 64, width, swiglu ? 64 : 128) >= 256)
+    if (rows > 64 * n) {
+        const TileSize size = best_tiles(r, width, swiglu ? 128 : 256, inner);
+        if (size == kLarge)
+            return swiglu ? start<kForwardGlu, 256, 256, 64, 2, 4, 2>(a, rows, stream)
+                          : start<kForward, 256, 256, 64, 2, 4, 2>(a, rows, stream);
+        if (size == kSquare)
+            return swiglu ? start<kForwardGlu, 128, 128, 64, 2, 2, 2>(a, rows, stream)
+                          : start<kForward, 128, 128, 64, 2, 2, 2>(a, rows, stream);
+    }
+    if (rows > 64 * n || (rows > 20 * n && tiles_of(r, 64, width, swiglu ? 64 : 128) >= 256))
         return swiglu ? start<kForwardGlu, 128, 64, 64, 3, 4, 1>(a, rows, stream)
                       : start<kForward, 128, 64, 64, 3, 4, 1>(a, rows, stream);
     return swiglu ? start<kForwardGlu, 128, 32, 64, 4, 4, 1>(a, rows, stream)
@@ -599,21 +611,17 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     a.sum = width;
     a.preact_in = (const uint16_t *)preact;
     a.out = dx;
-    // Measured, us, large / small tiles: 16 experts of 2048 x 7168, 16 rows
-    // each 84.5 / 87.1, 256 rows 131 / 198; 64 of 1024 x 2048, 16 rows 44.8 /
-    // 43.1, 96 rows 56 / 74; 16 of 512 x 1024 (64 to 128 large tiles), 256 rows
-    // 21.0 / 10.7, 384 rows 22.3 / 17.3. Large / square / small: 4 of 2600 rows,
-    // 656 x 1120 (210 large tiles, 738 square) 28.6 / 33.5 / 35.4; 8 of 1500
-    // rows, 1432 x 320 (100, 291) 37.8 / 28.3 / 30.5; 6 of 700 rows, 1200 x 704
-    // (57, 210) 33.0 / 21.1 / 18.6.
+    // Few rows an expert, us, large / small tiles: 16 experts of 2048 x 7168, 16
+    // rows each 84.5 / 87.1; 64 of 1024 x 2048, 16 rows 44.8 / 43.1.
     hipError_t status;
     if (preact ? start_split<kDgradGlu>(a, r.num_rows, stream, status)
                : start_split<kDgrad>(a, r.num_rows, stream, status))
         return status;
-    if (tiles_of(r, 256, inner, 256) >= kEnoughLarge)
+    const TileSize size = best_tiles(r, inner, 256, width);
+    if (size == kLarge)
         return preact ? start<kDgradGlu, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 256, 256, 64, 2, 4, 2>(a, r.num_rows, stream);
-    if (square_tiles(r, inner, 128))
+    if (size == kSquare)
         return preact ? start<kDgradGlu, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream);
     return preact ? start<kDgradGlu, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream)

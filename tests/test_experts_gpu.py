@@ -46,8 +46,8 @@ def untouched(t, off, cnt, name):
 
 
 # counts, gap between ranges, order of ranges in memory, width, inner. The
-# average rows per expert and the number of tiles choose the kernel; the large
-# ones need 256 tiles of 256 x 256 (the last three cases).
+# average rows per expert, the number of tiles and the length of the sum choose
+# the kernel: few rows or tiles the small ones, the last cases the larger ones.
 CASES = [
     ("one row", [1], 0, None, 8, 8),
     ("one row each", [1, 1, 1, 1], 0, None, 40, 72),
@@ -71,6 +71,7 @@ CASES = [
     ("middle, wide", [40, 0, 64, 65, 90, 31, 2, 130], 0, None, 2056, 2056),
     ("five experts, wide", [100, 0, 60, 200, 64], 0, None, 1032, 1032),
     ("few experts, many rows", [2100, 0, 1900], 0, None, 520, 2056),
+    ("24 experts, large tiles, every kind of last one", [(i * 53) % 300 for i in range(24)], 1, None, 2056, 2056),
     ("square tiles, odd sizes", [1500, 0, 901, 303], 1, None, 1800, 1672),
 ]
 IDS = [c[0] for c in CASES]
