@@ -81,6 +81,12 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
     static constexpr int kRing = kDeep ? 3 * kPBytes + 2 * kQBytes : S * (kPBytes + kQBytes);
     static constexpr int kLds = WK * kRing;
     static_assert(WK == 1 || !kDeep, "");
+    // A wave a SIMD: sums stay in the accumulation registers.
+    static constexpr bool kInPlace = !kDeep && kWaves * WK == 4 && kLds > 80 * 1024 && NI * NJ >= 16;
+    // Waves a SIMD: as LDS allows, but at least two: with all 512 registers to
+    // itself a wave's sums go to the accumulation registers and are moved to and
+    // fro in the loop (128 x 128 weight gradient: 88 moves for 16 instructions).
+    static constexpr int kPerSimd = 160 * 1024 / kLds * kWaves * WK / 4 > 2 ? 160 * 1024 / kLds * kWaves * WK / 4 : 2;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
     static_assert(!kGlu || NI % 2 == 0, "gate and up fragments pair up in a wave");
 
@@ -350,11 +356,17 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+                        for (int j = 0; j < NJ; ++j) {
+                            if constexpr (kInPlace)
+                                mfma_in_place(acc[i][j], pf[i], qf[j]);
+                            else
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
+                        }
                 }
                 buf = buf + 1 == S ? 0 : buf + 1;
             }
+            if constexpr (kInPlace)
+                mfma_settle();
         }
         drain_copies();
 
@@ -449,7 +461,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
 
 // The large tiles' kernels carry the smaller ones for an expert's last rows.
 template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK>
-__global__ __launch_bounds__(WP *WQ *WK *kWave) void gemm_kernel(Args a)
+__global__ __launch_bounds__(WP *WQ *WK *kWave, (Kernel<OP, TP, TQ, BK, S, WP, WQ, WK>::kPerSimd)) void gemm_kernel(Args a)
 {
     using K = Kernel<OP, TP, TQ, BK, S, WP, WQ, WK>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
@@ -640,31 +652,40 @@ hipError_t launch_expert_wgrad(const ExpertRows &r, const void *dy, const void *
     a.nq = width;
     a.out = dw;
     a.accumulate = accumulate;
-    // Large tiles for long sums and enough tiles; three workgroups of small
-    // ones share a CU, which covers the start and end of short sums. Measured,
-    // us, large / small: 16 experts of 2048 x 7168, 64 rows each 174 / 155
-    // (bf16), 213 / 185 (float32), 256 rows 263 / 243, 294 / 330, 1024 rows
-    // 519 / 569, 545 / 703; 64 of 1024 x 2048, 64 rows 105 / 85, 1024 rows
-    // 308 / 345; 8 of 512 x 1024 (64 large tiles), 1024 rows 31 / 20.
-    // Few tiles (a workgroup a CU at most): half as large ones, whose waves
-    // divide the sum among them, else four pairs of waves on a tile; the same
-    // for two rounds of workgroups if the sums are long. Against the small
-    // tiles: 2 experts of 376 x 648, 5200 rows each (132 tiles of 64 x 64) 29 /
-    // 68 (pairs 34), 4 of 512 x 512, 512 rows (256 tiles) 7.0 / 11.9 (8.0); 4 of
-    // 512 x 1024 (256 tiles of 128 x 64), 256 rows 7.8 / 9.2, 4096 rows 27.6 /
-    // 56.5 (64 x 64: 36); 8 of 512 x 1024, 1024 rows 21.3 / 20.8, 4096 rows 48.5
-    // / 57.2; 5 of 320 x 1432 (300), 800 rows 19.5 / 16.7, 3000 rows 40.4 / 42.1.
-    const auto tiles_of_size = [&](int w, int i) {
-        return (int64_t)((width + w - 1) / w) * ((inner + i - 1) / i) * r.n;
-    };
-    const int64_t mid = tiles_of_size(64, 128);
-    if (tiles_of_size(64, 64) <= 256)
+    // Few tiles, a workgroup a CU at most: 64 x 64 whose waves divide the sum
+    // among them, else 64 x 128 with four pairs of waves. Measured, us, 64 x 64 /
+    // 64 x 128 / 128 x 128: 2 experts of 376 x 648, 5200 rows each (132 tiles of
+    // 64 x 64) 29 / 34 / 68; 4 of 512 x 512, 512 rows (256) 7.0 / 8.0 / 11.9; 4
+    // of 512 x 1024 (256 of 64 x 128), 256 rows 10.2 / 7.3 / 9.1, 4096 rows 36 /
+    // 28 / 56.
+    const auto tiles = [&](int w, int i) { return (int64_t)((width + w - 1) / w) * ((inner + i - 1) / i) * r.n; };
+    if (tiles(64, 64) <= 256)
         return f32 ? start<kWgradF32, 64, 64, 64, 2, 1, 1, 4>(a, r.n, stream)
                    : start<kWgrad, 64, 64, 64, 2, 1, 1, 4>(a, r.n, stream);
-    if (mid <= 256 || (mid <= 512 && r.num_rows >= 1024 * (int64_t)r.n))
+    if (tiles(64, 128) <= 256)
         return f32 ? start<kWgradF32, 128, 64, 32, 3, 2, 1, 4>(a, r.n, stream)
                    : start<kWgrad, 128, 64, 32, 3, 2, 1, 4>(a, r.n, stream);
-    if (tiles_of_size(256, 256) >= 128 && r.num_rows >= 384 * (int64_t)r.n)
+    // Else large tiles (one a CU), small ones (128 x 128, three a CU, which
+    // covers the start and end of short sums), or those with two groups of waves
+    // (one a CU): what takes the least time by the rounds of workgroups and a
+    // round's time, about linear in the rows of an expert. Measured, us, large /
+    // small / two groups: 2 experts of 4624 x 368, 11246 rows each (222 small
+    // tiles) 137 / 143 / 113; 8 of 512 x 1024, 1024 rows (256) 31 / 18.8 / 15.3; 16
+    // of 512 x 1024, 128 rows (512) 16.4 / 10.7 / 14.7; 2 of 1408 x 2920, 647 rows
+    // (506) 28.2 / 20.2 / 25.6; 7 of 112 x 7160, 2136 rows (392) 55 / 43 / 54; 16 of
+    // 2048 x 7168, 64 rows 174 / 155 / -, 256 rows 259 / 238 / - (float32, whose
+    // rounds of many tiles write more, 296 / 316), 1024 rows 509 / 546 / - (float32
+    // 530 / 637); 64 of 1024 x 2048, 64 rows 105 / 82 / -, 1024 rows 306 / 331 / -.
+    const int64_t sum = r.num_rows / r.n, count = tiles(128, 128);
+    const auto rounds = [](int64_t t, int64_t slots) { return (t + slots - 1) / slots; };
+    // ns
+    const int64_t large = rounds(tiles(256, 256), 256) * (8000 + sum * 21);
+    const int64_t pairs = rounds(count, 256) * (3000 + sum * 17 / 2);
+    const int64_t small = count <= 512 ? 2500 + sum * 33 / 2 : rounds(count, 768) * ((f32 ? 5000 : 2500) + sum * 24);
+    if (pairs < small && pairs < large)
+        return f32 ? start<kWgradF32, 128, 128, 64, 2, 2, 2, 2>(a, r.n, stream)
+                   : start<kWgrad, 128, 128, 64, 2, 2, 2, 2>(a, r.n, stream);
+    if (large < small)
         return f32 ? start<kWgradF32, 256, 256, 64, 2, 4, 2>(a, r.n, stream)
                    : start<kWgrad, 256, 256, 64, 2, 4, 2>(a, r.n, stream);
     return f32 ? start<kWgradF32, 128, 128, 32, 3, 2, 2>(a, r.n, stream)

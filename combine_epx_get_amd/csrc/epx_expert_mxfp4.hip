@@ -57,6 +57,10 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
     static constexpr int kSCopies = (kScales + kWaves - 1) / kWaves;
     static constexpr int kBuf = kPBytes + kQBytes + kSCopies * kWaves * 256;
     static constexpr int kRing = S * kBuf, kLds = WK * kRing;
+    // Waves a SIMD: as LDS allows, but at least two: with all 512 registers to
+    // itself a wave's sums go to the accumulation registers, and every addition
+    // moves them to and fro.
+    static constexpr int kPerSimd = 160 * 1024 / kLds * kWaves * WK / 4 > 2 ? 160 * 1024 / kLds * kWaves * WK / 4 : 2;
     static constexpr int kLag = 3;
     static constexpr bool kAtOnce = WQ == 1 && SUBS * NI * NJ <= 16;
     static_assert(kPBytes % (1024 * kWaves) == 0 && kQBytes % (1024 * kWaves) == 0, "copies divide over the waves");
@@ -395,7 +399,7 @@ template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ
 };
 
 template <bool GLU, bool FP8OUT, int TP, int TQ, int SUBS, int S, int WP, int WQ, int WK>
-__global__ __launch_bounds__(WP *WQ *WK *kWave) void mx_kernel(Args a)
+__global__ __launch_bounds__(WP *WQ *WK *kWave, (Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ, WK>::kPerSimd)) void mx_kernel(Args a)
 {
     using K = Kernel<GLU, FP8OUT, TP, TQ, SUBS, S, WP, WQ, WK>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
