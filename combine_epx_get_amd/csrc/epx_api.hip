@@ -307,7 +307,9 @@ epx_status check_route(const Geometry &g, const void *logits, int32_t dtype, int
 // The experts' row ranges; `viol` is set by arm_rows.
 epx_status make_rows(const epx_expert_rows *r, epx::ExpertRows *out)
 {
-    if (!r || r->num_experts < 1 || r->num_experts > epx::kMaxExperts || r->num_rows < 0)
+    // a sum over rows looks some steps past its end, in 32 bits
+    constexpr int32_t kMostRows = INT32_MAX - 4095;
+    if (!r || r->num_experts < 1 || r->num_experts > epx::kMaxExperts || r->num_rows < 0 || r->num_rows > kMostRows)
         return EPX_ERR_ARG;
     if (!r->row_offset || !r->row_count || !aligned(r->row_offset, 4) || !aligned(r->row_count, 4))
         return EPX_ERR_ARG;

@@ -531,8 +531,8 @@ class ExpertRows:
         _need(row_count, torch.int32, "row_count", 1)
         if row_offset.numel() < row_count.numel() or row_offset.device != row_count.device:
             raise ValueError("row_offset: need an entry for every expert of row_count, on its device")
-        if not 0 <= num_rows < 1 << 31:
-            raise ValueError("num_rows: need 0 <= num_rows < 2^31")
+        if not 0 <= num_rows <= (1 << 31) - 4096:
+            raise ValueError("num_rows: need 0 <= num_rows <= 2^31 - 4096")
         self.row_offset, self.row_count = row_offset, row_count
         self.num_experts, self.num_rows, self.device = row_count.numel(), int(num_rows), row_count.get_device()
         self.struct = epx_expert_rows(self.num_experts, self.num_rows, row_offset.data_ptr(), row_count.data_ptr())

@@ -416,7 +416,7 @@ EPX_API epx_status epx_combine_backward(const epx_problem *p, const epx_layout *
  * are neither read nor written. A range that is not inside [0, num_rows)
  * counts as empty (the bounds-checked build counts it, see
  * epx_checked_violations).
- * Limits: 1 <= num_experts <= 2048, 0 <= num_rows < 2^31. */
+ * Limits: 1 <= num_experts <= 2048, 0 <= num_rows <= 2^31 - 4096. */
 typedef struct {
     int32_t num_experts;
     int32_t num_rows;            /* rows of the buffers that the ranges address */

@@ -86,7 +86,7 @@ def test_combine_backward(epx, lib):
 
 
 BAD_ROWS = [dict(n=0), dict(n=-1), dict(n=2049), dict(R=-1), dict(off=None), dict(cnt=None), dict(off=A + 2),
-            dict(cnt=A + 1)]
+            dict(cnt=A + 1), dict(R=2 ** 31 - 4095), dict(R=2 ** 31 - 1)]
 # width, inner (of a product whose matrix has `wide` rows)
 BAD_SIZES = [(0, 64), (4, 64), (12, 64), (-8, 64), (64, 0), (64, 12), (64, -8), ((1 << 20) + 8, 8), (8, (1 << 20) + 8),
              (65536, 16392)]
