@@ -556,7 +556,12 @@ bool start_split(const Args &a, int64_t rows, hipStream_t stream, hipError_t &st
 // 19 / 20 / 17. Gradient of the input: 2 of 11246 rows, 4624 x 368 107 / 144 /
 // 144; 4 of 2600, 656 x 1120 29 / 34 / 35; 8 of 1500, 1432 x 320 38 / 28 / 31;
 // 6 of 700, 1200 x 704 33 / 21 / 19.
-enum TileSize { kLarge, kSquare, kSmall };
+// At most one small tile a CU and a sum of 1024 or more: two groups of waves
+// divide it (kSmallSplit), us, against one: 1 expert of 4096 rows, 512 x 4096
+// (256 tiles) 26.5 / 31.2; 2 of 647, 1408 x 2920 (231) 27.5 / 27.7; gradient of
+// the input, 1 of 3000, 7168 x 512 (188) 42.7 / 51.8; 16 of 96, 2048 x 1024
+// (256) 17.3 / 18.8; but 8 of 300, 1000 x 1000 (328) 22.3 / 18.3.
+enum TileSize { kLarge, kSquare, kSmall, kSmallSplit };
 TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, int64_t sum)
 {
     auto rounds = [&](int height, int width, int64_t slots) {
@@ -566,7 +571,11 @@ TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, in
     const int64_t large = rounds(256, 256, 256) * (9000 + sum * 47 / 2);
     const int64_t square = rounds(128, 128, 512) * (4500 + sum * 33 / 2);
     const int64_t small = rounds(64, 128, 512) * (4200 + sum * 63 / 5);
-    return large <= square && large <= small ? kLarge : square <= small ? kSquare : kSmall;
+    if (large <= square && large <= small)
+        return kLarge;
+    if (square <= small)
+        return kSquare;
+    return sum >= 1024 && tiles_of(r, 64, columns, columns_of_256 / 2) <= 256 ? kSmallSplit : kSmall;
 }
 
 }  // namespace
@@ -604,6 +613,9 @@ hipError_t launch_expert_gemm(const ExpertRows &r, const void *x, const void *w,
         if (size == kSquare)
             return swiglu ? start<kForwardGlu, 128, 128, 64, 2, 2, 2>(a, rows, stream)
                           : start<kForward, 128, 128, 64, 2, 2, 2>(a, rows, stream);
+        if (size == kSmallSplit)
+            return swiglu ? start<kForwardGlu, 128, 64, 64, 3, 4, 1, 2>(a, rows, stream)
+                          : start<kForward, 128, 64, 64, 3, 4, 1, 2>(a, rows, stream);
     }
     if (rows > 64 * n || (rows > 20 * n && tiles_of(r, 64, width, swiglu ? 64 : 128) >= 256))
         return swiglu ? start<kForwardGlu, 128, 64, 64, 3, 4, 1>(a, rows, stream)
@@ -636,6 +648,9 @@ hipError_t launch_expert_dgrad(const ExpertRows &r, const void *dy, const void *
     if (size == kSquare)
         return preact ? start<kDgradGlu, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream)
                       : start<kDgrad, 128, 128, 64, 2, 2, 2>(a, r.num_rows, stream);
+    if (size == kSmallSplit)
+        return preact ? start<kDgradGlu, 128, 64, 64, 3, 4, 1, 2>(a, r.num_rows, stream)
+                      : start<kDgrad, 128, 64, 64, 3, 4, 1, 2>(a, r.num_rows, stream);
     return preact ? start<kDgradGlu, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream)
                   : start<kDgrad, 128, 64, 64, 3, 4, 1>(a, r.num_rows, stream);
 }

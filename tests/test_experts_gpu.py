@@ -71,6 +71,7 @@ CASES = [
     ("middle, wide", [40, 0, 64, 65, 90, 31, 2, 130], 0, None, 2056, 2056),
     ("five experts, wide", [100, 0, 60, 200, 64], 0, None, 1032, 1032),
     ("few experts, many rows", [2100, 0, 1900], 0, None, 520, 2056),
+    ("four experts, long sums", [900, 0, 33, 700], 0, None, 1096, 1096),
     ("24 experts, large tiles, every kind of last one", [(i * 53) % 300 for i in range(24)], 1, None, 2056, 2056),
     ("square tiles, odd sizes", [1500, 0, 901, 303], 1, None, 1800, 1672),
 ]
