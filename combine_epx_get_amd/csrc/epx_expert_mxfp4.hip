@@ -436,12 +436,9 @@ hipError_t start(Args a, hipStream_t stream)
 
 template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stream)
 {
-    // As the bf16 products, with other borders. Measured, us, large / 64 rows
-    // / 32 rows, gated: 16 experts of 2048 x 7168, 16 rows each 51 / 56 / 45,
-    // 48 rows 52 / 60 / 69, 128 rows 74 / 113 / 134; 64 of 1024 x 2048, 32 rows
-    // 32 / 34 / 29, 48 rows 34 / 35 / 44; 16 of 512 x 1024 (64 to 128 large
-    // tiles), 64 rows 9.8 / 8.9 / 9.0, 192 rows 19.2 / 11.1 / 12.7, 384 rows
-    // 20.2 / 17.0 / 21.9.
+    // Measured, us, large / 64 rows / 32 rows, gated: 16 experts of 2048 x 7168,
+    // 16 rows each 51 / 56 / 45, 48 rows 52 / 60 / 69, 128 rows 74 / 113 / 134; 64
+    // of 1024 x 2048, 32 rows 32 / 34 / 29, 48 rows 34 / 35 / 44.
     const int64_t rows = a.r.num_rows, n = a.r.n;
     // Where small tiles would leave CUs idle: the largest tile of which there
     // are at most 256, one workgroup a CU whose waves divide the sum among
@@ -466,6 +463,32 @@ template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stre
             return start<GLU, FP8OUT, 64, 32, 1, 3, 1, 1, 6>(a, stream);
         if (tiles_of(a.r, 64, a.np, 2 * kFull) <= 256)
             return start<GLU, FP8OUT, 64, 64, 1, 3, 1, 1, 4>(a, stream);
+    }
+    // From 64 rows an expert large tiles, square ones of 128 (two a CU) or
+    // small ones: what takes the least time by the rounds of workgroups and a
+    // round's time, as in the bf16 products (16 experts of 2048 rows and 2048
+    // columns, sums of 256 / 1024 / 4096: large 52 / 90 / 267 us, square 46 / 96
+    // / 350, small, whose round is put a quarter higher, 83 / 135 / 475). Large /
+    // square / small elsewhere: 13 of 917 rows, 1064 x 1536 50 / 34 / 44; 3 of
+    // 6887, gated 176 x 3968 54 / 47 / 61; 16 of 256, 2048 x 1024 24 / 17 / 21; 4
+    // of 1000, 512 x 7168 83 / 48 / 31; 64 of 96, gated 1024 x 2048 49 / 44 / 57.
+    // (The columns of gated fp8 rows out do not divide into square tiles.)
+    if constexpr (!(GLU && FP8OUT)) {
+        if (rows > 64 * n) {
+            const auto rounds = [&](int height, int columns, int64_t slots) {
+                return (tiles_of(a.r, height, a.np, GLU ? columns / 2 : columns) + slots - 1) / slots;
+            };
+            // ns
+            const int64_t sum = a.sum;
+            const int64_t large = rounds(256, 256, 256) * (7200 + sum * 71 / 5);
+            const int64_t square = rounds(128, 128, 512) * (2400 + sum * 10);
+            const int64_t small = rounds(64, 128, 512) * (3750 + sum * 8);
+            if (square < large && square < small)
+                return start<GLU, FP8OUT, 128, 128, 1, 2, 2, 2>(a, stream);
+            if (small < large)
+                return start<GLU, FP8OUT, 128, 64, 1, 4, 4, 1>(a, stream);
+            return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 4>(a, stream);
+        }
     }
     if (rows > 28 * n && tiles_of(a.r, 256, a.np, GLU ? 128 : 256) >= 256)
         return start<GLU, FP8OUT, 256, 256, 1, 3, 2, 4>(a, stream);

@@ -95,7 +95,9 @@ def test_dequantise_every_code_and_scale(epx):
 CASES = [(n, c, gap, o, N, 128 * (1 + (K // 72) % 9)) for n, c, gap, o, N, K in BF16_CASES] + [
     ("few tiles, 21 blocks", [33, 0, 64, 7], 1, None, 264, 2688),
     ("some tiles, 29 blocks", [100, 0, 60, 150], 0, None, 520, 3712),
-    ("more tiles, 23 blocks", [290, 2, 260], 2, [2, 0, 1], 808, 2944)]
+    ("more tiles, 23 blocks", [290, 2, 260], 2, [2, 0, 1], 808, 2944),
+    ("24 experts, 13 blocks", [(i * 53) % 300 for i in range(24)], 1, None, 1032, 1664),
+    ("24 experts, wide, 13 blocks", [(i * 53) % 300 for i in range(24)], 1, None, 2056, 1664)]
 
 
 def operands(g, n, M, R, K, epx):
@@ -133,7 +135,8 @@ def test_product(epx, case, act):
                                   ("large tiles", [(i * 53) % 300 for i in range(150)], 1, None, 384, 256),
                                   ("few rows, 60 experts", [i % 5 for i in range(60)], 0, None, 256, 640),
                                   ("middle, wide", [40, 64, 0, 130, 200, 61, 150, 55], 0, None, 1536, 384),
-                                  ("few tiles, 21 blocks", [70, 3], 1, None, 256, 2688)],
+                                  ("few tiles, 21 blocks", [70, 3], 1, None, 256, 2688),
+                                  ("24 experts, wide", [(i * 53) % 300 for i in range(24)], 1, None, 2176, 1664)],
                          ids=lambda c: c[0])
 def test_product_to_fp8_rows(epx, case, act):
     name, cnt, gap, order, N, K = case
