@@ -307,8 +307,12 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                     for (int c = i * kQPer; c < (i + 1) * kQPer && c < kQCopies; ++c)
                         copy_q(c, q0);
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
+                    for (int j = 0; j < NJ; ++j) {
+                        if (i == NI - 1 && j == NJ - 1)
+                            mfma_in_place_last(acc[i][j], pf[1][i], qf[1][j], uniform(steps - 1 - step));
+                        else
+                            mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 const uint32_t free_p = p0, free_q = q0;
@@ -318,7 +322,6 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                 q0 = q1;
                 q1 = free_q;
             }
-            mfma_settle();
         } else {
             auto issue = [&](int step, int buf) {
                 const uint32_t at = lds + (uint32_t)buf * (kPBytes + kQBytes);
@@ -357,16 +360,17 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                     for (int i = 0; i < NI; ++i)
 #pragma unroll
                         for (int j = 0; j < NJ; ++j) {
-                            if constexpr (kInPlace)
-                                mfma_in_place(acc[i][j], pf[i], qf[j]);
-                            else
+                            if constexpr (kInPlace) {
+                                if (s == BK / 32 - 1 && i == NI - 1 && j == NJ - 1)
+                                    mfma_in_place_last(acc[i][j], pf[i], qf[j], uniform(own_steps - 1 - step));
+                                else
+                                    mfma_in_place(acc[i][j], pf[i], qf[j]);
+                            } else
                                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[i], qf[j], acc[i][j], 0, 0, 0);
                         }
                 }
                 buf = buf + 1 == S ? 0 : buf + 1;
             }
-            if constexpr (kInPlace)
-                mfma_settle();
         }
         drain_copies();
 

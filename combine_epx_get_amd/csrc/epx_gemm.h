@@ -103,15 +103,29 @@ template <typename T> __device__ __forceinline__ T lds_read(uint32_t at)
 // to itself the compiler moves sums that fill all 256 of them between the two
 // register files inside the loop. It does not know this for a matrix
 // instruction, so nothing but another one (of another sum, or at least four
-// later) may follow until mfma_settle().
+// later) may touch a sum until mfma_in_place_last() has waited.
 __device__ __forceinline__ void mfma_in_place(f32x4 &c, bf16x8 a, bf16x8 b)
 {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// After the last of them, before the sums are read: the longest wait that a
-// result of a 16x16 instruction can need.
-__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// The last of a step. Where no step follows (more is 0), it waits in the same
+// statement for the longest time that a result of a 16x16 instruction can
+// need, so that whatever reads, copies or spills a sum behind the loop finds
+// it done. A statement of its own behind the loop does not order that: the
+// compiler read sums, and with the sums as its operands copied them, ahead of
+// it, 11 to 18 wait states after the last instruction.
+__device__ __forceinline__ void mfma_in_place_last(f32x4 &c, bf16x8 a, bf16x8 b, int more)
+{
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\t"
+                 "s_cmp_lg_u32 %3, 0\n\t"
+                 "s_cbranch_scc1 2\n\t"   // over the two waits
+                 "s_nop 15\n\t"
+                 "s_nop 15"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "s"(more)
+                 : "scc");
+}
 
 // Sums of WK groups of waves that divided a tile's sum: every group's go to its
 // RING bytes of LDS, and each of them adds up, in the order of the groups, NE
