@@ -7,7 +7,9 @@ of gfx950: 5 between a vector instruction that writes a scalar register and a
 memory instruction that reads it, 2 between one that writes a vector register
 and a matrix instruction that reads it, and up to 19 between a matrix
 instruction and any other use of its result (16 passes; a wait is one
-instruction, or n + 1 for "s_nop n"). Needs the compiler, no GPU."""
+instruction, or n + 1 for "s_nop n"). The copies also set m0, which a statement
+cannot name among what it changes: nothing else may use it. Needs the
+compiler, no GPU."""
 import os
 import re
 import subprocess
@@ -190,6 +192,7 @@ def test_waits_around_assembly_statements(assembly):
         kernels += 1
         copies += sum(1 for op, _, inside in code if inside and op.startswith("buffer_"))
         products += sum(1 for op, _, inside in code if inside and op.startswith("v_mfma"))
+        assert not [c for c in code if not c[2] and "m0" in c[1]], name
         early = faults(blocks)
         if early:
             bad[name] = sorted(early)[:4]
