@@ -327,9 +327,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
             e = -1;
         else {
             le = Row<TIn>::get(row + e);
-            g = scale * dweights[t * k + lane];
+            // a masked choice's weight is 0 whatever the logits: its gradient
+            // (which may be infinite or NaN) reaches nothing
+            if (!masked(le))
+                g = scale * dweights[t * k + lane];
         }
     }
+    const bool on = !masked(le);
     float d[PER];   // every expert's gradient before the chosen ones' part
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -349,21 +353,20 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
         sum = token_sum<L>(sum);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         const float p = exp_to(le, m) * inv;
-        c = e >= 0 ? g * p : 0.0f;
+        c = on ? g * p : 0.0f;
         const float all = token_sum<L>(c);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            d[i] = -(exp_to(l[i], m) * inv) * all;
+            d[i] = masked(l[i]) ? 0.0f : -(exp_to(l[i], m) * inv) * all;
     } else if (softmax) {
         const float m = token_maxf<L>(le);
-        const float x = e >= 0 ? exp_to(le, m) : 0.0f;
+        const float x = on ? exp_to(le, m) : 0.0f;
         const float sum = token_sum<L>(x);
         const float p = sum > 0.0f ? x / sum : 0.0f;
-        const float mean = token_sum<L>(e >= 0 ? g * p : 0.0f);
-        c = e >= 0 ? p * (g - mean) : 0.0f;
+        const float mean = token_sum<L>(on ? g * p : 0.0f);
+        c = on ? p * (g - mean) : 0.0f;
     } else {
         // 1 - p is formed as 1 / (1 + exp(l)): p alone loses it near 1
-        const bool on = e >= 0 && !masked(le);
         const double p = on ? sigmoid64(le) : 0.0, q = on ? 1.0 / (1.0 + exp((double)le)) : 0.0;
         if (renormalize) {
             const double sum = token_sum<L>(p);

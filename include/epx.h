@@ -388,8 +388,9 @@ EPX_API epx_status epx_route(const epx_problem *p, const void *logits, int32_t l
 /* Gradient of epx_route's weights: dlogits [T, E] (logits_dtype, every
  * element written) from dweights float32 [T, k] and the ids that epx_route
  * chose. The choice itself has no gradient (nor has the bias); masked experts
- * get 0. An id outside [0, E) contributes nothing; an id that is given twice
- * counts twice. Errors: EPX_ERR_ARG. */
+ * get 0, and what dweights holds at a masked choice is not used (it may be
+ * infinite or NaN). An id outside [0, E) contributes nothing; an id that is
+ * given twice counts twice. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_route_backward(const epx_problem *p, const void *logits,
                                       int32_t logits_dtype, int32_t score, int32_t renormalize,
                                       float scale, const int32_t *topk_idx, const float *dweights,

@@ -1,0 +1,53 @@
+"""The router and its gradient where masks meet infinite or NaN gradients."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_route_gpu import as_input, epx, gradient  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+KINDS = ["softmax", "softmax_all", "sigmoid", "sigmoid_all"]
+
+
+def backward(epx, p, t, score, idx, dw, renorm, scale=1.0):  # noqa: F811
+    d = torch.full_like(t, -9.0)
+    epx.epx_route_backward(p, t, score, idx, dw, d, renormalize=renorm, scale=scale)
+    torch.cuda.synchronize()
+    return d
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("E,k", [(40, 8), (200, 40), (300, 8), (1500, 40)])
+def test_gradients_of_masked_choices_reach_nothing(epx, E, k, kind, dtype):  # noqa: F811
+    """Tokens with fewer live experts than k choose masked ones, whose weights are 0: what stands at those places of
+    dweights changes nothing, and a masked expert's gradient is 0 whatever the live choices' are."""
+    rng = np.random.default_rng(E + k)
+    l = rng.standard_normal((9, E))
+    l[:, 5:] = -np.inf
+    l[1, 2], l[2, :4], l[3, :] = np.nan, -np.inf, np.nan
+    t, l = as_input(l, dtype)
+    softmax, renorm = kind.startswith("softmax"), not kind.endswith("_all")
+    score = epx.SCORE_SOFTMAX if softmax else epx.SCORE_SIGMOID
+    p = epx.make_problem(9, k, E, 1, 1)
+    idx, w = torch.empty(9, k, dtype=torch.int32, device="cuda"), torch.empty(9, k, device="cuda")
+    epx.epx_route(p, t, score, idx, w, renormalize=renorm)
+    dead = torch.from_numpy(~(l > -np.inf)).cuda()
+    chosen_dead = dead.gather(1, idx.long())
+    assert not w[chosen_dead].any() and int(chosen_dead.sum()) >= 9 * (k - 5)
+    dw = torch.from_numpy(rng.standard_normal((9, k)).astype(np.float32)).cuda()
+    dw[chosen_dead] = 0.0
+    want = backward(epx, p, t, score, idx, dw, renorm)
+    ref, size = gradient(l, idx.cpu().numpy(), dw.double().cpu().numpy(), softmax, renorm, 1.0)
+    # as in the router's other tests: terms of the largest |dw|, and half a step of the type
+    tol = 2.0 ** -23 * (16 + 4 * 5 + E) * dw.abs().max(1, keepdim=True).values.double().cpu().numpy()
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    assert np.all(np.abs(want.double().cpu().numpy() - ref) <= tol + half * (np.abs(ref) + tol) + 1e-37)
+    for bad in (float("nan"), float("inf"), float("-inf"), 3e38):
+        dw2 = dw.clone()
+        dw2[chosen_dead] = bad
+        assert torch.equal(backward(epx, p, t, score, idx, dw2, renorm, 2.5), backward(epx, p, t, score, idx, dw, renorm, 2.5)), bad
+    for bad in (float("nan"), float("inf")):
+        dw2 = dw.clone()
+        dw2[~chosen_dead] = bad
+        assert not backward(epx, p, t, score, idx, dw2, renorm)[dead].any(), bad
