@@ -182,7 +182,8 @@ __global__ __launch_bounds__(256) void route_kernel(const TIn *__restrict__ logi
         id[i] = at + i;
         if (BIASED) {
             const double key = in ? sigmoid64(l[i]) + (double)bias[at + i] : 0.0;
-            // a NaN or -infinity bias masks like such a logit
+            // a NaN or -infinity bias ranks like such a logit (the weight is
+            // the score's all the same)
             const bool none = masked(l[i]) || !(key > -__builtin_inf());
             const uint64_t s = sortable(key);
             hi[i] = !in ? kTaken : none ? kMasked : (uint32_t)(s >> 32);

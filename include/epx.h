@@ -377,7 +377,10 @@ EPX_API epx_status epx_plan_swaps(int32_t num_experts, int32_t num_ranks, int32_
  * A logit of -infinity or NaN masks its expert: score 0, chosen (in order of
  * id) only when a token has fewer than k others. A token with nothing left
  * gets weights 0. Masked experts rank below every other one, whatever their
- * bias. A softmax over logits of +infinity shares the weight among them.
+ * bias. A bias of -infinity or NaN ranks its expert among the masked ones, but
+ * only that: chosen because a token has fewer than k others, it has its
+ * score's weight and gradient (mask the logit to give an expert none). A
+ * softmax over logits of +infinity shares the weight among them.
  * Errors: EPX_ERR_ARG. */
 typedef enum { EPX_SCORE_SOFTMAX = 0, EPX_SCORE_SIGMOID = 1 } epx_score;
 

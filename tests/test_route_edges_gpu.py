@@ -1,9 +1,10 @@
-"""The router and its gradient where masks meet infinite or NaN gradients."""
+"""The router and its gradient where masks meet infinite or NaN gradients and
+biases."""
 import numpy as np
 import pytest
 import torch
 
-from tests.test_route_gpu import as_input, epx, gradient  # noqa: F401
+from tests.test_route_gpu import as_input, epx, gradient, run, run_backward, scores  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 KINDS = ["softmax", "softmax_all", "sigmoid", "sigmoid_all"]
@@ -51,3 +52,34 @@ def test_gradients_of_masked_choices_reach_nothing(epx, E, k, kind, dtype):  # n
         dw2 = dw.clone()
         dw2[~chosen_dead] = bad
         assert not backward(epx, p, t, score, idx, dw2, renorm)[dead].any(), bad
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(70, 8), (200, 40), (600, 12)])
+def test_bias_of_minus_infinity_or_nan_orders_only(epx, E, k, renorm, dtype):  # noqa: F811
+    """Such an expert comes after every other one, with the masked ones in order of id; chosen all the same, it has its
+    score's weight and gradient."""
+    rng = np.random.default_rng(E * 3 + k)
+    t, l = as_input(rng.standard_normal((6, E)), dtype)
+    l[2, ::2], l[3, 1::2] = -np.inf, np.nan
+    t, l = as_input(l, dtype)
+    b = rng.standard_normal(E).astype(np.float32)
+    b[6:] = -np.inf
+    b[8::3] = np.nan
+    b[E - 2] = 0.25
+    p = epx.make_problem(6, k, E, 1, 1)
+    idx, w = torch.empty(6, k, dtype=torch.int32, device="cuda"), torch.empty(6, k, device="cuda")
+    epx.epx_route(p, t, epx.SCORE_SIGMOID, idx, w, bias=torch.from_numpy(b).cuda(), renormalize=renorm, scale=2.5)
+    torch.cuda.synchronize()
+    sc = scores(l, False)
+    key = sc + b.astype(np.float64)
+    key = np.where((l > -np.inf) & (key > -np.inf), key, -np.inf)
+    want = np.argsort(-key, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(idx.cpu().numpy(), want)
+    # at most 7 experts have a bias that is a number
+    c = np.take_along_axis(sc, want, 1)
+    assert (c[:, 7:] > 0).any() and (np.take_along_axis(l, want, 1)[2] == -np.inf).any()
+    s = c.sum(1, keepdims=True)
+    assert np.all(np.abs(w.cpu().numpy() - 2.5 * (c / s if renorm else c)) <= 2.0 ** -20 * 2.5 * (c / s if renorm else c))
+    run_backward(epx, p, t, l, idx, epx.SCORE_SIGMOID, False, renorm, 2.5, E)
