@@ -1,5 +1,5 @@
 """The router and its gradient where masks meet infinite or NaN gradients and
-biases."""
+biases, and with more choices than half a wave has lanes."""
 import numpy as np
 import pytest
 import torch
@@ -83,3 +83,22 @@ def test_bias_of_minus_infinity_or_nan_orders_only(epx, E, k, renorm, dtype):  #
     s = c.sum(1, keepdims=True)
     assert np.all(np.abs(w.cpu().numpy() - 2.5 * (c / s if renorm else c)) <= 2.0 ** -20 * 2.5 * (c / s if renorm else c))
     run_backward(epx, p, t, l, idx, epx.SCORE_SIGMOID, False, renorm, 2.5, E)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS + ["biased"])
+@pytest.mark.parametrize("shape", [(4, 40, 40), (5, 33, 33), (7, 64, 64), (3, 65, 34), (9, 100, 40), (6, 128, 33), (11, 256, 64),
+                                   (1, 200, 47)], ids=str)
+def test_more_than_32_choices_of_up_to_256_experts(epx, shape, kind, dtype):  # noqa: F811
+    """Two choices a lane forwards, a whole wave a token backwards; with masked tokens of fewer than k experts."""
+    T, E, k = shape
+    rng = np.random.default_rng(T * 10007 + E * 101 + k)
+    l = 1.5 * rng.standard_normal((T, E))
+    l[0, rng.permutation(E)[:E - 20]] = -np.inf
+    if T > 3:
+        l[1], l[2, 10:] = np.nan, -np.inf
+        l[3] = np.round(l[3])   # ties
+    softmax, renorm = kind.startswith("softmax"), not kind.endswith("_all")
+    bias = 0.2 * rng.standard_normal(E) if kind == "biased" else None
+    p, t, l, idx, score = run(epx, l, dtype, k, softmax, bias, renorm, 2.5)
+    run_backward(epx, p, t, l, idx, score, softmax, renorm, 2.5, E)
