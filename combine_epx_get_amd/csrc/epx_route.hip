@@ -438,10 +438,8 @@ template <typename F> void with_shape(int E, int k, F f)
         f(std::integral_constant<int, 2>(), part);
     } else if (E <= 4 * 32) {
         f(std::integral_constant<int, 4>(), part);
-    } else if (E <= 8 * 32) {
-        f(std::integral_constant<int, 8>(), part);
     } else {
-        f(std::integral_constant<int, 16>(), part);
+        f(std::integral_constant<int, 8>(), part);
     }
 }
 
