@@ -123,8 +123,7 @@ hipError_t launch_combine_backward(const Geometry &g, const epx_layout &L, const
     }
     int threads = (nvec + kWave - 1) / kWave * kWave;
     threads = threads > 512 ? 512 : threads;
-    if (threads < g.k)
-        threads = (g.k + kWave - 1) / kWave * kWave;
+    static_assert(kMaxTopk <= kWave, "a thread a choice, from the first wave");
     const dim3 grid = item_grid(g.T, (g.k + per - 1) / per);
     if (dw)
         launch(combine_backward_kernel<true>, grid, dim3(threads), 0, stream, (const u32x4 *)dout,
