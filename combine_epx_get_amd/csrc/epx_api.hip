@@ -3,6 +3,7 @@
 // fails a check launches nothing.
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "epx_internal.h"
@@ -339,6 +340,16 @@ bool product_sizes_ok(int64_t rows, int32_t width, int32_t inner, int32_t unit_i
 
 bool ready(const void *p, uintptr_t a) { return p && aligned(p, a); }
 
+// An output that starts where one of the other buffers does: workgroups would
+// read what others have written.
+bool in_place(const void *out, std::initializer_list<const void *> others)
+{
+    for (const void *o : others)
+        if (out && out == o)
+            return true;
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -666,7 +677,8 @@ epx_status epx_route(const epx_problem *p, const void *logits, int32_t logits_dt
         return EPX_ERR_ARG;
     if (g.T == 0)
         return EPX_OK;
-    if (!ready(topk_idx, 4) || !ready(topk_weights, 4))
+    if (!ready(topk_idx, 4) || !ready(topk_weights, 4) ||
+        in_place(topk_idx, {logits, bias, topk_weights}) || in_place(topk_weights, {logits, bias}))
         return EPX_ERR_ARG;
     return from_hip(epx::launch_route(g, logits, logits_dtype == EPX_BF16,
                                       score == EPX_SCORE_SOFTMAX, bias, renormalize != 0, scale,
@@ -687,7 +699,8 @@ epx_status epx_route_backward(const epx_problem *p, const void *logits, int32_t 
         return st;
     if (g.T == 0)
         return EPX_OK;
-    if (!ready(topk_idx, 4) || !ready(dweights, 4) || !ready(dlogits, 16) || dlogits == logits)
+    if (!ready(topk_idx, 4) || !ready(dweights, 4) || !ready(dlogits, 16) ||
+        in_place(dlogits, {logits, topk_idx, dweights}))
         return EPX_ERR_ARG;
     return from_hip(epx::launch_route_backward(g, logits, logits_dtype == EPX_BF16,
                                                score == EPX_SCORE_SOFTMAX, renormalize != 0, scale,
@@ -711,9 +724,10 @@ epx_status epx_combine_backward(const epx_problem *p, const epx_layout *layout, 
         return EPX_ERR_CAPACITY;
     if (g.T == 0)
         return EPX_OK;
-    if (!ready(dout, 16) || !ready(dy, 16) || !ready(topk_weights, 4) || dy == y || dy == dout)
+    if (!ready(dout, 16) || !ready(dy, 16) || !ready(topk_weights, 4) ||
+        in_place(dy, {y, dout, topk_weights, dweights}))
         return EPX_ERR_ARG;
-    if (dweights && (!ready(y, 16) || !aligned(dweights, 4)))
+    if (dweights && (!ready(y, 16) || !aligned(dweights, 4) || in_place(dweights, {dout, y, topk_weights})))
         return EPX_ERR_ARG;
     if ((st = arm_checks(g)) != EPX_OK)
         return st;
@@ -738,7 +752,8 @@ epx_status epx_expert_gemm(const epx_expert_rows *rows, const void *x, const voi
         return EPX_ERR_ARG;
     if (r.num_rows == 0)
         return EPX_OK;
-    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || out == x || out == preact)
+    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || in_place(out, {x, w, preact}) ||
+        in_place(preact, {x, w}))
         return EPX_ERR_ARG;
     if ((st = arm_rows(r)) != EPX_OK)
         return st;
@@ -762,7 +777,7 @@ epx_status epx_expert_gemm_dgrad(const epx_expert_rows *rows, const void *dy, co
     if (r.num_rows == 0)
         return EPX_OK;
     if (!ready(dy, 16) || !ready(w, 16) || !ready(dx, 16) || (glu && !ready(preact, 16)) ||
-        dx == dy || dx == preact)
+        in_place(dx, {dy, w, preact}))
         return EPX_ERR_ARG;
     if ((st = arm_rows(r)) != EPX_OK)
         return st;
@@ -782,7 +797,7 @@ epx_status epx_expert_gemm_wgrad(const epx_expert_rows *rows, const void *dy, co
     if ((dw_dtype != EPX_BF16 && dw_dtype != EPX_F32) || (accumulate != 0 && accumulate != 1) ||
         (accumulate && dw_dtype != EPX_F32) || !product_sizes_ok(width, width, inner, 8))
         return EPX_ERR_ARG;
-    if (!ready(dw, 16) || (r.num_rows > 0 && (!ready(dy, 16) || !ready(x, 16))))
+    if (!ready(dw, 16) || (r.num_rows > 0 && (!ready(dy, 16) || !ready(x, 16) || in_place(dw, {dy, x}))))
         return EPX_ERR_ARG;
     if ((st = arm_rows(r)) != EPX_OK)
         return st;
@@ -798,7 +813,7 @@ epx_status epx_mxfp4_quantize(const void *x, int64_t num_rows, int32_t inner, ui
         return EPX_ERR_ARG;
     if (num_rows == 0)
         return EPX_OK;
-    if (!ready(x, 16) || !ready(codes, 16) || !scales)
+    if (!ready(x, 16) || !ready(codes, 16) || !scales || in_place(codes, {x, scales}) || in_place(scales, {x}))
         return EPX_ERR_ARG;
     return from_hip(
         epx::launch_mxfp4_quantize(x, num_rows, inner, codes, scales, (hipStream_t)stream));
@@ -812,7 +827,7 @@ epx_status epx_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int
         return EPX_ERR_ARG;
     if (num_rows == 0)
         return EPX_OK;
-    if (!ready(out, 16) || !ready(codes, 16) || !scales)
+    if (!ready(out, 16) || !ready(codes, 16) || !scales || in_place(out, {codes, scales}))
         return EPX_ERR_ARG;
     return from_hip(
         epx::launch_mxfp4_dequantize(codes, scales, num_rows, inner, out, (hipStream_t)stream));
@@ -836,7 +851,9 @@ epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint8_t *x,
     if (r.num_rows == 0)
         return EPX_OK;
     if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || !ready(x_scales, 4) ||
-        !ready(w_scales, 4) || (fp8 && !ready(out_scales, 4)) || out == x)
+        !ready(w_scales, 4) || (fp8 && !ready(out_scales, 4)) ||
+        in_place(out, {x, x_scales, w, w_scales}) ||
+        (fp8 && in_place(out_scales, {x, x_scales, w, w_scales, out})))
         return EPX_ERR_ARG;
     if ((st = arm_rows(r)) != EPX_OK)
         return st;

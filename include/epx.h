@@ -362,6 +362,11 @@ EPX_API epx_status epx_plan_swaps(int32_t num_experts, int32_t num_ranks, int32_
                                   int32_t *rank_load_before, int32_t *rank_load_after,
                                   int32_t *swaps, int32_t *host_bad, void *stream);
 
+/* ---- Buffers of the calls from here to epx_expert_gemm_mxfp4: what a call
+ * writes must not overlap anything else that it is given. An output that
+ * starts where another buffer does is refused (EPX_ERR_ARG); other overlaps
+ * are not looked for. ---- */
+
 /* ---- Router. Scores, choice and weights of the k experts of every token,
  * as epx_get_layout and epx_combine take them. The problem gives T, E and k
  * (k <= 64, E <= 2048; its ranks, hosts, mode and groups play no part).
@@ -442,7 +447,7 @@ typedef enum { EPX_ACT_NONE = 0, EPX_ACT_SWIGLU = 1 } epx_act;
  * Products are summed in float32 and rounded once, to bf16 (nearest even);
  * the activation is computed from the float32 sums. width and inner are
  * multiples of 8 of at most 2^20, rows of one expert's matrix times inner at
- * most 2^30; every pointer is 16-byte aligned. The buffers must not overlap.
+ * most 2^30; every pointer is 16-byte aligned.
  * Errors: EPX_ERR_ARG; EPX_ERR_DEVICE also for more tiles than one launch
  * can have (2^32 threads). */
 EPX_API epx_status epx_expert_gemm(const epx_expert_rows *rows, const void *x, const void *w,
@@ -507,7 +512,7 @@ EPX_API epx_status epx_mxfp4_dequantize(const uint8_t *codes, const uint8_t *sca
  * Sums in float32: every 128 channels of codes, then times the row's scale.
  * inner is a multiple of 128, width of 8 (of 128 for fp8 rows out), rows of
  * one expert's matrix times inner at most 2^30; x, w, out are 16-byte
- * aligned, the scales to 4 bytes. The buffers must not overlap. Errors: EPX_ERR_ARG. */
+ * aligned, the scales to 4 bytes. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint8_t *x,
                                          const float *x_scales, const uint8_t *w,
                                          const uint8_t *w_scales, int32_t width, int32_t inner,
