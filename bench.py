@@ -115,15 +115,11 @@ def relay_receive_bytes(T, k, H, hidden, rows, fp8, f32_partials):
 
 def kernel_sources_hash(kernel: str = "") -> str:
     """Hash of the source file holding `kernel` (plus the shared internal
-    headers); of every kernel source when the kernel is not listed."""
-    csrc = os.path.join(ROOT, "combine_epx_get_amd", "csrc")
-    if kernel in KERNEL_SOURCE:
-        files = [os.path.join(csrc, f) for f in (KERNEL_SOURCE[kernel], "epx_internal.h", "epx_device.h")]
-    else:
-        files = sorted(glob.glob(os.path.join(csrc, "*")))
+    headers); of every source that holds a measured kernel when the kernel is not listed."""
+    sources = [KERNEL_SOURCE[kernel]] if kernel in KERNEL_SOURCE else sorted(set(KERNEL_SOURCE.values()))
     h = hashlib.sha256()
-    for f in files:
-        h.update(open(f, "rb").read())
+    for f in (*sources, "epx_internal.h", "epx_device.h"):
+        h.update(open(os.path.join(ROOT, "combine_epx_get_amd", "csrc", f), "rb").read())
     return h.hexdigest()[:16]
 
 
@@ -196,8 +192,8 @@ def ingest_trace(stats_csv: str, tag: str, command: str) -> str:
     import csv
     rows = list(csv.DictReader(open(stats_csv)))
     out = [f"# {tag}: rocprofv3 kernel trace", "",
-           f"sources_hash: {kernel_sources_hash()} (every file of combine_epx_get_amd/csrc; bench.py "
-           f"reports these averages only while the sources hash to it)", "",
+           f"sources_hash: {kernel_sources_hash()} (bench.py's kernel_sources_hash(): the sources of the kernels it "
+           f"measures; it reports these averages only while they hash to it)", "",
            "Command ($REPO is the repository root, run on an MI355X):", "", "    " + command, "",
            "| kernel | calls | average µs | min µs | max µs | % of GPU time |", "|---|---|---|---|---|---|"]
     for r in rows:

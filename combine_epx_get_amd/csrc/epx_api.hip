@@ -6,7 +6,7 @@
 #include <initializer_list>
 #include <mutex>
 
-#include "epx_internal.h"
+#include "epx_operators.h"
 
 // Scratch of epx_layout_dispatch_noalloc: the layout workspace for callers
 // that cannot allocate. One copy per GPU (each device holds its own at its

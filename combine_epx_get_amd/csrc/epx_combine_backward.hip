@@ -12,6 +12,7 @@
 // A dot product is summed in a fixed order that depends on the launch shape
 // only: ascending chunks in each lane, lanes by xor, waves ascending.
 #include "epx_device.h"
+#include "epx_operators.h"
 
 namespace epx {
 namespace {

@@ -12,7 +12,6 @@ __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }
 // up (lanes below n in the row read 0: bound_ctrl); row_bcast:15 / 31 hand
 // lane 15 / 31 to the next row(s), written only where row_mask allows.
 constexpr int kDppRowShr = 0x110;
-constexpr int kDppRowRor = 0x120;   // row_ror:n rotates each row's values by n lanes
 constexpr int kDppRowBcast15 = 0x142;
 constexpr int kDppRowBcast31 = 0x143;
 

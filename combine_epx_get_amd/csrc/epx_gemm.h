@@ -7,6 +7,7 @@
 #pragma once
 
 #include "epx_device.h"
+#include "epx_operators.h"
 
 namespace epx {
 

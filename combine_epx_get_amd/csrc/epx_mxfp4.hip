@@ -9,6 +9,7 @@
 // HBM bound: 2 + 17/32 bytes an element in either direction (65536 x 7168,
 // both directions: 343-368 us, 6.5 to 6.9 TB/s; 2048 x 7168: 13.5 us).
 #include "epx_device.h"
+#include "epx_operators.h"
 
 namespace epx {
 namespace {

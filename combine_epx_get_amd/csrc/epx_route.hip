@@ -18,11 +18,13 @@
 // float32, take 9.4 us, the gradient 7.9 (17 and 34 MB). A biased choice is
 // bound by its double precision exponentials there (21 us).
 #include "epx_device.h"
+#include "epx_operators.h"
 
 namespace epx {
 namespace {
 
 constexpr uint32_t kTaken = 0, kMasked = 1;
+constexpr int kDppRowRor = 0x120;   // row_ror:n rotates each row's values by n lanes
 
 // Order-preserving integer of a number that is neither NaN nor -infinity
 // (those have smaller values than any of these); -0 counts as +0.
