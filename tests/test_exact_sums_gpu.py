@@ -155,3 +155,54 @@ def test_fp8_rows_out(epx, case):  # noqa: F811
     v = out[live].view(torch.float8_e4m3fn).double().view_as(zb) * s.double().unsqueeze(2)
     # the quotient's rounding to float32, then half a step: 2^-4 of the value, 2^-10 below the normal numbers
     assert bool(((v - zb).abs() <= zb.abs() * (2.0 ** -4 + 2.0 ** -23) + s.double().unsqueeze(2) * 2.0 ** -10).all())
+
+
+def window(places, values, big):
+    """One row and one column of 256 codes: `big` = 4 * x at place 0 and taken off again at place 128, and
+    0.5 * values[i] at places[i]; the result without the pair, in float64, and the operands."""
+    x, w = torch.zeros(1, 256, device="cuda"), torch.zeros(256, dtype=torch.long, device="cuda")
+    x[0, 0], x[0, 128], w[0], w[128] = big / 4, big / 4, 6, 14
+    x[0, places], w[places] = torch.tensor(values, device="cuda"), 1
+    q = x.to(torch.float8_e4m3fn)
+    codes = (w[0::2] | (w[1::2] << 4)).to(torch.uint8).expand(1, 8, 128).contiguous()
+    scales = torch.full((1, 8, 8), 127, dtype=torch.uint8, device="cuda")
+    return q.view(torch.uint8), torch.ones(1, 2, device="cuda"), codes, scales, 0.5 * q[0, places].double().sum()
+
+
+@pytest.mark.parametrize("place", [1, 5, 7, 8, 15, 16, 31, 32, 64, 100, 127, 129, 135, 136])
+def test_what_the_matrix_instruction_cuts(epx, place):  # noqa: F811
+    """Beside 2^10 in the same eight of a sum a product keeps its bits from 2^-3 on; elsewhere all of them that a
+    float32 sum of 2^10 holds."""
+    rows = make_rows(epx, [0], [1], 1)
+    near = place // 8 in (0, 16)
+    for value in (2.0 ** -2, 1.75, 2.0 ** -3, 1.125 * 2.0 ** -2, 1.875 * 2.0 ** -5, 2.0 ** -6, 13.0, -(2.0 ** -2), -1.875 * 2.0 ** -3):
+        x, xs, w, ws, want = window([place], [value], 1024.0)
+        out = guard(1, 8)
+        epx.epx_expert_gemm_mxfp4(rows, x, xs, w, ws, out)
+        torch.cuda.synchronize()
+        unit = 2.0 ** -3 if near else 2.0 ** -13
+        assert torch.equal(out[0].double(), (torch.trunc(want / unit) * unit).expand(8)), (place, value)
+
+
+def test_bound_of_the_cut(epx):  # noqa: F811
+    """Any operands: the result is off by less than 7 * 2^-13 of the largest product of every eight, and float32's sums."""
+    g = ex.gen(40, "cuda")
+    R, N, K = 48, 72, 1024
+    rows = make_rows(epx, [0], [R], R)
+    far = torch.exp2(torch.randint(-8, 9, (R, K), generator=g, device="cuda").float())
+    x = (torch.randn(R, K, generator=g, device="cuda") * far).clamp(-448, 448)
+    # the second half takes the first half's sum away: the same products in other eights
+    x[:, K // 2:] = x[:, :K // 2].roll(4, 1)
+    x = x.to(torch.float8_e4m3fn)
+    w = torch.randint(0, 16, (1, N, K // 2), generator=g, device="cuda")
+    w = torch.cat((w, w.roll(4, 2) ^ 8), 2)
+    codes = (w[..., 0::2] | (w[..., 1::2] << 4)).to(torch.uint8)
+    scales = torch.full((1, N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    out = guard(R, N)
+    epx.epx_expert_gemm_mxfp4(rows, x.view(torch.uint8), torch.ones(R, K // 128, device="cuda"), codes, scales, out)
+    torch.cuda.synchronize()
+    p = x.double()[:, None, :] * ref.mxfp4_values(codes, scales)[0][None]
+    want = p.sum(2)
+    largest = p.abs().view(R, N, K // 8, 8).amax(3).sum(2)
+    bound = 7 * 2.0 ** -13 * largest + K / 8 * 2.0 ** -24 * p.abs().sum(2)
+    assert bool(((out.double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound)).all())
