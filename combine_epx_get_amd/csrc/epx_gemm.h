@@ -324,6 +324,11 @@ inline int64_t tiles_of(const ExpertRows &r, int height, int64_t columns, int ti
 }
 
 // ---------------------------------------------------------------- activation
+// The hardware's reciprocal and base-2 exponential, a step or two each, and
+// the rounding of v * log2(e), which grows with v: 2^-22 * (1 + |v|) relative to
+// the value at most, far below the bf16 (or E4M3) step of what it is used for.
+// Below -87 the reciprocal is subnormal and comes back as 0: silu, which is
+// then less than 2^-119, is 0.
 __device__ __forceinline__ float sigmoid32(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 __device__ __forceinline__ float swiglu(float gate, float up) { return gate * sigmoid32(gate) * up; }
 

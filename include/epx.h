@@ -434,7 +434,8 @@ typedef struct {
 } epx_expert_rows;
 
 /* EPX_ACT_SWIGLU: the product has 2 * width columns, gates then ups, and the
- * output is silu(gate) * up = gate / (1 + exp(-gate)) * up. */
+ * output is silu(gate) * up = gate / (1 + exp(-gate)) * up (silu of a gate
+ * below -87, which is less than 2^-119, is 0). */
 typedef enum { EPX_ACT_NONE = 0, EPX_ACT_SWIGLU = 1 } epx_act;
 
 /* out[r, :] = act( x[r, :] * w[e]^T ) for every row r of expert e.

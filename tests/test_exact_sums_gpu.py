@@ -206,3 +206,33 @@ def test_bound_of_the_cut(epx):  # noqa: F811
     largest = p.abs().view(R, N, K // 8, 8).amax(3).sum(2)
     bound = 7 * 2.0 ** -13 * largest + K / 8 * 2.0 ** -24 * p.abs().sum(2)
     assert bool(((out.double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound)).all())
+
+
+def test_gates_far_below_zero(epx):  # noqa: F811
+    """silu and its gradient for gates down to -400: below -87 the reciprocal is no
+    normal float32 number any more and the result is 0, which is off by less than 88 * 2^-126 < 2^-119 times the other factors."""
+    gates = -torch.cat((torch.arange(0, 128, device="cuda") * 1.0, 80 + torch.arange(0, 40, device="cuda") * 0.5,
+                        torch.tensor([150.0, 200.0, 400.0], device="cuda"))).to(torch.bfloat16)
+    R, N, K = gates.numel(), 40, 8
+    rows = make_rows(epx, [0], [R], R)
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = gates, 1.0
+    ups = (torch.arange(N, device="cuda") - 20.0).to(torch.bfloat16)
+    w = torch.zeros(1, 2 * N, K, dtype=torch.bfloat16, device="cuda")
+    w[0, :N, 0], w[0, N:, 1] = 1.0, ups
+    out, pre = guard(R, N), guard(R, 2 * N)
+    epx.epx_expert_gemm(rows, x, w, out, act=epx.ACT_SWIGLU, preact=pre)
+    torch.cuda.synchronize()
+    same(pre, torch.cat((gates.double()[:, None].expand(R, N), ups.double().expand(R, N)), 1), "preact")
+    z = pre.double()
+    lost = 2.0 ** -119 * (ups.double().abs() + 1)
+    a, b = ref.glu(z, torch.zeros_like(z))
+    ref.close(out, a, b + lost, ref.BF16, "out")
+    # the gradient of preact for d = 3
+    dy, wd = torch.full((R, 8), 3.0, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 8, N, dtype=torch.bfloat16, device="cuda")
+    wd[0, 0] = 1.0
+    dx = guard(R, 2 * N)
+    epx.epx_expert_gemm_dgrad(rows, dy, wd, dx, input_act=epx.ACT_SWIGLU, preact=pre)
+    torch.cuda.synchronize()
+    d, bd = ref.glu_backward(torch.full((R, N), 3.0, dtype=torch.float64, device="cuda"), torch.zeros(R, N, dtype=torch.float64, device="cuda"), z)
+    ref.close(dx, d, bd + 3 * torch.cat((lost, lost)), ref.BF16, "dx")
