@@ -26,11 +26,14 @@
 // (lane / 16) on. Tiles, copies, ring of buffers and chunk permutation as in
 // the bf16 products; the scales come to LDS beside the codes.
 //
-// Few rows an expert: a CU's rate of reading bounds it (64 rows over 8 experts
-// of 2 x 2048 x 7168: 28.7 us, of which about 8 do not depend on the size).
-// Many: the matrix cores, whose clock falls to 1.5 GHz under these
-// instructions (32768 ragged rows, 16 experts of 2 x 2048 x 7168: 888-922 us,
-// 2.1 PFLOP/s; a library product of E4M3 with E4M3 reached 2.7 at 8192^3).
+// Few rows an expert (64 rows over 8 experts of 2 x 2048 x 7168): 28-29 us, of
+// which 20.6 are the weights at the read rate and about 6 the copies of the
+// scales (23.4 us with those left out): 4 bytes a lane from rows that are inner /
+// 32 bytes apart, so that nearly every lane asks for a cache line of its own.
+// Many (32768 ragged rows, 16 experts of 2 x 2048 x 7168): 888-935 us, 2.1 PFLOP/s
+// (812 without the scales' copies); the matrix cores are 50-57 % busy at 1.5
+// GHz and the waves wait 29 % of their time (a library product of E4M3 with
+// E4M3 reached 2.7 PFLOP/s at 8192^3).
 #include "epx_gemm.h"
 
 namespace epx {
@@ -461,6 +464,14 @@ template <bool GLU, bool FP8OUT> hipError_t pick(const Args &a, hipStream_t stre
     // 10.2. fp8 rows out, whose scale blocks need 128 columns a tile: 4 of 256
     // rows, 512 x 2048 (136 tiles) 8.7 / 13.1; 1 of 1 row, gated 2048 x 7168
     // (16) 26.6 / 34.1, but 8 of 8 rows (128) 38.4 / 35.9.
+    // Gated fp8 rows out (which the rule of rounds below leaves out), us, 256 /
+    // 64 / 32 rows / 32 rows divided: 8 experts of 2048 x 7168, 8 rows each 54 /
+    // 60 / 44 / 49, 32 rows 55 / 60 / 46 / 50, 96 rows 67 / 62 / 83 / 90, 256 rows 96 /
+    // 115 / 160 / 178; 16 of them, 48 rows 67 / 71 / 87 / 96, 128 rows 84 / 123 / 163
+    // / 182, 2048 rows 890 / 1799 / 2244 / 2880; 64 of 1024 x 2048, 16 rows 40 / 44 /
+    // 35 / 38, 96 rows 54 / 82 / 88 / 91; 4 of 1000 rows, 512 x 7168 89 / 58 / 72 / 81;
+    // 2 of 400 rows, 256 x 1024 21 / 13 / 9.3 / 8.4; 1 of 8 rows 37 / 51 / 34 / 34. The
+    // rule takes the best or is within 9 %, but at 8 experts of 256 rows (115).
     if constexpr (FP8OUT) {
         const int64_t tiles = tiles_of(a.r, 32, a.np, 128);
         if (tiles <= 32 || (tiles <= 256 && rows > 28 * n))

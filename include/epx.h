@@ -424,7 +424,10 @@ EPX_API epx_status epx_combine_backward(const epx_problem *p, const epx_layout *
  * gaps and come in any order but must not overlap. Rows outside every range
  * are neither read nor written. A range that is not inside [0, num_rows)
  * counts as empty (the bounds-checked build counts it, see
- * epx_checked_violations).
+ * epx_checked_violations). The counts are not known to the host, which
+ * chooses the kernels' tiles by num_rows: ranges that cover a small part of
+ * the buffers (one group's of several) are computed right but with tiles for
+ * more rows than they have.
  * Limits: 1 <= num_experts <= 2048, 0 <= num_rows <= 2^31 - 4096. */
 typedef struct {
     int32_t num_experts;
