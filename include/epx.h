@@ -428,7 +428,10 @@ EPX_API epx_status epx_combine_backward(const epx_problem *p, const epx_layout *
  * chooses the kernels' tiles by num_rows: ranges that cover a small part of
  * the buffers (one group's of several) are computed right but with tiles for
  * more rows than they have.
- * Limits: 1 <= num_experts <= 2048, 0 <= num_rows <= 2^31 - 4096. */
+ * Limits: 1 <= num_experts <= 2048, 0 <= num_rows <= 2^31 - 4096. A product
+ * or input gradient that could have more tiles than one launch takes (2^32
+ * threads, at least 2 a row: above about 10^9 rows) returns EPX_ERR_DEVICE and
+ * launches nothing. */
 typedef struct {
     int32_t num_experts;
     int32_t num_rows;            /* rows of the buffers that the ranges address */
@@ -452,8 +455,7 @@ typedef enum { EPX_ACT_NONE = 0, EPX_ACT_SWIGLU = 1 } epx_act;
  * the activation is computed from the float32 sums. width and inner are
  * multiples of 8 of at most 2^20, rows of one expert's matrix times inner at
  * most 2^30; every pointer is 16-byte aligned.
- * Errors: EPX_ERR_ARG; EPX_ERR_DEVICE also for more tiles than one launch
- * can have (2^32 threads). */
+ * Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm(const epx_expert_rows *rows, const void *x, const void *w,
                                    int32_t width, int32_t inner, int32_t act, void *preact,
                                    void *out, void *stream);
