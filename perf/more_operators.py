@@ -104,10 +104,10 @@ def _ranges(case, g):
 
 
 def _rows_int8(x):
-    """Rows in int8: a float32 scale max|x| / 127 (at least 2^-126; 0 for a row of zeros) and the nearest integers of
+    """Rows in int8: a float32 scale max|x| / 127 (at least 2^-125; 0 for a row of zeros) and the nearest integers of
     the quotients, ties to even. A quotient next to a tie needs more than 32 bits; 64 tell all of them."""
     amax = x.float().abs().amax(-1)
-    s = torch.where(amax > 0, (amax / 127.0).clamp(min=2.0 ** -126), 0.0)
+    s = torch.where(amax > 0, (amax / 127.0).clamp(min=2.0 ** -125), 0.0)
     q = torch.round(x.double() / torch.where(s > 0, s, 1.0).double().unsqueeze(-1))
     return q.clamp(-127, 127).to(torch.int8), s
 
@@ -303,7 +303,7 @@ def exact(case, seed):
         for part in st["x"].split(4096):
             v = part.double()
             # the scale is a float32 number by definition
-            s = torch.clamp(torch.linalg.vector_norm(v, float("inf"), dim=1) / 127.0, min=2.0 ** -126).float().double()
+            s = torch.clamp(torch.linalg.vector_norm(v, float("inf"), dim=1) / 127.0, min=2.0 ** -125).float().double()
             s = torch.where((v == 0).all(1), 0.0, s)
             a = v.abs() / torch.where(s > 0, s, 1.0).unsqueeze(1)
             low = torch.floor(a)
