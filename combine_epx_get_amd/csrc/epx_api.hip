@@ -338,6 +338,13 @@ bool product_sizes_ok(int64_t rows, int32_t width, int32_t inner, int32_t unit_i
            inner % unit_inner == 0 && inner <= kMost && rows * inner <= ((int64_t)1 << 30);
 }
 
+// Sizes of rows converted to 8 bits and back.
+bool rows8_ok(int64_t num_rows, int32_t inner, int32_t unit)
+{
+    return num_rows >= 0 && num_rows < ((int64_t)1 << 31) && inner >= unit && inner % unit == 0 &&
+           inner <= 1 << 20;
+}
+
 bool ready(const void *p, uintptr_t a) { return p && aligned(p, a); }
 
 // An output that starts where one of the other buffers does: workgroups would
@@ -859,6 +866,169 @@ epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint8_t *x,
         return st;
     return from_hip(epx::launch_expert_gemm_mxfp4(r, x, x_scales, w, w_scales, width, inner, glu,
                                                   fp8, out, out_scales, (hipStream_t)stream));
+}
+
+epx_status epx_int8_quantize(const void *x, int64_t num_rows, int32_t inner, int8_t *codes,
+                             float *scales, void *stream)
+{
+    HookScope hook_scope;
+    if (!rows8_ok(num_rows, inner, 16))
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(codes, 16) || !ready(scales, 4) || in_place(codes, {x, scales}) ||
+        in_place(scales, {x}))
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_int8_quantize(x, num_rows, inner, codes, scales, (hipStream_t)stream));
+}
+
+epx_status epx_int8_dequantize(const int8_t *codes, const float *scales, int64_t num_rows,
+                               int32_t inner, void *out, void *stream)
+{
+    HookScope hook_scope;
+    if (!rows8_ok(num_rows, inner, 16))
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(out, 16) || !ready(codes, 16) || !ready(scales, 4) || in_place(out, {codes, scales}))
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_int8_dequantize(codes, scales, num_rows, inner, out, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_int8(const epx_expert_rows *rows, const int8_t *x,
+                                const float *x_scales, const int8_t *w, const float *w_scales,
+                                int32_t width, int32_t inner, int32_t act, int8_t *preact_codes,
+                                uint8_t *preact_scales, void *out, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    const bool glu = act == EPX_ACT_SWIGLU;
+    // a sum of inner products of at most 2^14 stays below 2^31
+    constexpr int32_t kMostInner = (1 << 17) - 16;
+    if ((act != EPX_ACT_NONE && !glu) || inner > kMostInner ||
+        !product_sizes_ok(glu ? (int64_t)2 * width : width, width, inner, 16))
+        return EPX_ERR_ARG;
+    if ((preact_codes != nullptr) != (preact_scales != nullptr) ||
+        (preact_codes && (!glu || width % 32 != 0 || !aligned(preact_codes, 16))))
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || !ready(x_scales, 4) ||
+        !ready(w_scales, 16) ||
+        in_place(out, {x, x_scales, w, w_scales, preact_codes, preact_scales}) ||
+        in_place(preact_codes, {x, x_scales, w, w_scales, preact_scales}) ||
+        in_place(preact_scales, {x, x_scales, w, w_scales}))
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_gemm_int8(r, x, x_scales, w, w_scales, width, inner, glu,
+                                                 preact_codes, preact_scales, out,
+                                                 (hipStream_t)stream));
+}
+
+epx_status epx_mxint8_quantize(const void *x, int64_t num_rows, int32_t inner, int8_t *codes,
+                               uint8_t *scales, void *stream)
+{
+    HookScope hook_scope;
+    if (!rows8_ok(num_rows, inner, 32))
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(codes, 16) || !scales || in_place(codes, {x, scales}) ||
+        in_place(scales, {x}))
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_mxint8_quantize(x, num_rows, inner, codes, scales, (hipStream_t)stream));
+}
+
+epx_status epx_mxint8_dequantize(const int8_t *codes, const uint8_t *scales, int64_t num_rows,
+                                 int32_t inner, void *out, void *stream)
+{
+    HookScope hook_scope;
+    if (!rows8_ok(num_rows, inner, 32))
+        return EPX_ERR_ARG;
+    if (num_rows == 0)
+        return EPX_OK;
+    if (!ready(out, 16) || !ready(codes, 16) || !scales || in_place(out, {codes, scales}))
+        return EPX_ERR_ARG;
+    return from_hip(
+        epx::launch_mxint8_dequantize(codes, scales, num_rows, inner, out, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_keep8(const epx_expert_rows *rows, const void *x, const void *w,
+                                 int32_t width, int32_t inner, int8_t *preact_codes,
+                                 uint8_t *preact_scales, void *out, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    if (!product_sizes_ok((int64_t)2 * width, width, inner, 8) || width % 32 != 0)
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(x, 16) || !ready(w, 16) || !ready(out, 16) || !ready(preact_codes, 16) ||
+        !preact_scales || in_place(out, {x, w, preact_codes, preact_scales}) ||
+        in_place(preact_codes, {x, w, preact_scales}) || in_place(preact_scales, {x, w}))
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_gemm_keep8(r, x, w, width, inner, preact_codes,
+                                                  preact_scales, out, (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_dgrad_kept8(const epx_expert_rows *rows, const void *dy, const void *w,
+                                       int32_t width, int32_t inner, const int8_t *preact_codes,
+                                       const uint8_t *preact_scales, void *act_out, void *dx,
+                                       void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    if (!product_sizes_ok(width, width, inner, 32) || (act_out && !aligned(act_out, 16)))
+        return EPX_ERR_ARG;
+    if (r.num_rows == 0)
+        return EPX_OK;
+    if (!ready(dy, 16) || !ready(w, 16) || !ready(dx, 16) || !ready(preact_codes, 16) ||
+        !preact_scales || in_place(dx, {dy, w, preact_codes, preact_scales, act_out}) ||
+        in_place(act_out, {dy, w, preact_codes, preact_scales}))
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_dgrad_kept8(r, dy, w, width, inner, preact_codes,
+                                                   preact_scales, act_out, dx,
+                                                   (hipStream_t)stream));
+}
+
+epx_status epx_expert_gemm_wgrad_kept8(const epx_expert_rows *rows, const void *dy,
+                                       const int8_t *x_codes, const uint8_t *x_scales,
+                                       int32_t width, int32_t inner, int32_t dw_dtype,
+                                       int32_t accumulate, void *dw, void *stream)
+{
+    HookScope hook_scope;
+    epx::ExpertRows r;
+    epx_status st = make_rows(rows, &r);
+    if (st != EPX_OK)
+        return st;
+    if ((dw_dtype != EPX_BF16 && dw_dtype != EPX_F32) || (accumulate != 0 && accumulate != 1) ||
+        (accumulate && dw_dtype != EPX_F32) || !product_sizes_ok(width, width, inner, 32))
+        return EPX_ERR_ARG;
+    if (!ready(dw, 16) || (r.num_rows > 0 && (!ready(dy, 16) || !ready(x_codes, 16) || !x_scales ||
+                                              in_place(dw, {dy, x_codes, x_scales}))))
+        return EPX_ERR_ARG;
+    if ((st = arm_rows(r)) != EPX_OK)
+        return st;
+    return from_hip(epx::launch_expert_wgrad_kept8(r, dy, x_codes, x_scales, width, inner,
+                                                   dw_dtype == EPX_F32, accumulate != 0, dw,
+                                                   (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,37 @@
+// epx_expert_int8.hip -- the experts' products of int8 rows and int8 weights,
+// with a float32 scale per row and per column, on the matrix cores of gfx950.
+//
+//   z[r, n] = fl32(sum_k x[r, k] w[e][n, k]) * x_scale[r] * w_scale[e][n]
+//
+// The tile loop of the bf16 products: a 16-byte chunk holds 16 values in place
+// of 8, the matrix instruction (16x16x64) takes chunks as the bf16 one
+// (16x16x32) does and multiplies twice the values in the same cycles. Sums are
+// whole numbers in 32 bits, exact up to the inner limit of epx.h, so neither
+// tiles nor groups of waves change a result; scales, activation and the 8-bit
+// form of the pre-activations are applied to them before the one rounding.
+#include "epx_expert_tiles.h"
+
+namespace epx {
+
+hipError_t launch_expert_gemm_int8(const ExpertRows &r, const int8_t *x, const float *x_scales,
+                                   const int8_t *w, const float *w_scales, int32_t width,
+                                   int32_t inner, bool swiglu, int8_t *kept, uint8_t *kept_scales,
+                                   void *out, hipStream_t stream)
+{
+    Args8 a = {};
+    a.r = r;
+    a.p = (const char *)w;
+    a.q = (const char *)x;
+    a.np = width;
+    a.sum = inner / 2;
+    a.out = out;
+    a.q_scales = x_scales;
+    a.p_scales = w_scales;
+    a.kept = kept;
+    a.kept_scales = kept_scales;
+    if (kept)
+        return start_forward<kInt8Keep>(a, stream);
+    return swiglu ? start_forward<kInt8Glu>(a, stream) : start_forward<kInt8>(a, stream);
+}
+
+}  // namespace epx

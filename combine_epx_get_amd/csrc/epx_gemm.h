@@ -47,6 +47,12 @@ __device__ __forceinline__ i32x4 buffer_of(const char *base, uint32_t bytes)
     return r;
 }
 
+// The same for the compiler's own loads.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t read_buffer(const char *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)uniform_ptr(base), 0, uniform((int)bytes), 0x00020000);
+}
+
 __device__ __forceinline__ uint32_t lds_offset(const void *p)
 {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
@@ -110,6 +116,11 @@ __device__ __forceinline__ void mfma_in_place(f32x4 &c, bf16x8 a, bf16x8 b)
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
+__device__ __forceinline__ void mfma_in_place(i32x4 &c, bf16x8 a, bf16x8 b)
+{
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
 // The last of a step. Where no step follows (more is 0), it waits in the same
 // statement for the longest time that a result of a 16x16 instruction can
 // need, so that whatever reads, copies or spills a sum behind the loop finds
@@ -128,13 +139,25 @@ __device__ __forceinline__ void mfma_in_place_last(f32x4 &c, bf16x8 a, bf16x8 b,
                  : "scc");
 }
 
+__device__ __forceinline__ void mfma_in_place_last(i32x4 &c, bf16x8 a, bf16x8 b, int more)
+{
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0\n\t"
+                 "s_cmp_lg_u32 %3, 0\n\t"
+                 "s_cbranch_scc1 2\n\t"
+                 "s_nop 15\n\t"
+                 "s_nop 15"
+                 : "+a"(c)
+                 : "v"(a), "v"(b), "s"(more)
+                 : "scc");
+}
+
 // Sums of WK groups of waves that divided a tile's sum: every group's go to its
 // RING bytes of LDS, and each of them adds up, in the order of the groups, NE
 // of the NJ columns of fragments, from j0 = group * NE on (groups past the
 // last get none). WAVES waves a group; the groups' copies have arrived.
-template <int WK, int RING, int WAVES, int NI, int NJ, int NE>
-__device__ __forceinline__ void join_groups(uint32_t lds, int group, int wave, const f32x4 (&acc)[NI][NJ],
-                                            f32x4 (&all)[NI][NE])
+template <int WK, int RING, int WAVES, int NI, int NJ, int NE, typename V>
+__device__ __forceinline__ void join_groups(uint32_t lds, int group, int wave, const V (&acc)[NI][NJ],
+                                            V (&all)[NI][NE])
 {
     static_assert(NJ % NE == 0 && WK * NE >= NJ && RING >= WAVES * NI * NJ * kWave * 16, "");
     auto at = [&](int of, int i, int j) {
@@ -146,7 +169,7 @@ __device__ __forceinline__ void join_groups(uint32_t lds, int group, int wave, c
     for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            *(__attribute__((address_space(3))) f32x4 *)(uintptr_t)at(group, i, j) = acc[i][j];
+            *(__attribute__((address_space(3))) V *)(uintptr_t)at(group, i, j) = acc[i][j];
     __syncthreads();
     const int j0 = group * NE;
     if (j0 >= NJ)
@@ -155,10 +178,10 @@ __device__ __forceinline__ void join_groups(uint32_t lds, int group, int wave, c
     for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            all[i][j] = lds_read<f32x4>(at(0, i, j0 + j));
+            all[i][j] = lds_read<V>(at(0, i, j0 + j));
 #pragma unroll
             for (int of = 1; of < WK; ++of)
-                all[i][j] += lds_read<f32x4>(at(of, i, j0 + j));
+                all[i][j] += lds_read<V>(at(of, i, j0 + j));
         }
 }
 
@@ -314,6 +337,15 @@ __device__ __forceinline__ void merge_columns(f32x4 &a, f32x4 &b)
     }
 }
 
+// The largest of what the four lanes m, m + 16, m + 32 and m + 48 hold.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t v)
+{
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const uint32_t w = max((uint32_t)h[0], (uint32_t)h[1]);
+    const auto x = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return max((uint32_t)x[0], (uint32_t)x[1]);
+}
+
 // Tiles of `height` rows and `tile_columns` columns that a product has with
 // its experts equally full, each with a last tile half full.
 inline int64_t tiles_of(const ExpertRows &r, int height, int64_t columns, int tile_columns)
@@ -364,6 +396,20 @@ __device__ __forceinline__ void store_f32(float *row, int c, int width, const Co
             const f32x4 x = {o.v[i], o.v[i + 1], o.v[i + 2], o.v[i + 3]};
             *d = add ? *d + x : x;
         }
+}
+
+// The same read from a float32 row; 0 past its columns.
+template <int N> __device__ __forceinline__ Cols<N> load_f32(const float *row, int c, int width)
+{
+    Cols<N> o;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const f32x4 x = c + i < width ? *(const f32x4 *)(row + c + i) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            o.v[i + q] = x[q];
+    }
+    return o;
 }
 
 // Columns [c, c + N) of a bf16 row; 0 past its `width` columns.

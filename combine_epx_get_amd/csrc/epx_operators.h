@@ -47,4 +47,30 @@ hipError_t launch_mxfp4_quantize(const void *x, int64_t num_rows, int32_t inner,
 hipError_t launch_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t num_rows,
                                    int32_t inner, void *out, hipStream_t stream);
 
+// 8 bits: rows and back, products of int8, and products that write or read
+// activations kept in 8 bits. kept: may be null for the int8 product; act:
+// may be null.
+hipError_t launch_int8_quantize(const void *x, int64_t num_rows, int32_t inner, int8_t *codes,
+                                float *scales, hipStream_t stream);
+hipError_t launch_int8_dequantize(const int8_t *codes, const float *scales, int64_t num_rows,
+                                  int32_t inner, void *out, hipStream_t stream);
+hipError_t launch_mxint8_quantize(const void *x, int64_t num_rows, int32_t inner, int8_t *codes,
+                                  uint8_t *scales, hipStream_t stream);
+hipError_t launch_mxint8_dequantize(const int8_t *codes, const uint8_t *scales, int64_t num_rows,
+                                    int32_t inner, void *out, hipStream_t stream);
+hipError_t launch_expert_gemm_int8(const ExpertRows &r, const int8_t *x, const float *x_scales,
+                                   const int8_t *w, const float *w_scales, int32_t width,
+                                   int32_t inner, bool swiglu, int8_t *kept, uint8_t *kept_scales,
+                                   void *out, hipStream_t stream);
+hipError_t launch_expert_gemm_keep8(const ExpertRows &r, const void *x, const void *w,
+                                    int32_t width, int32_t inner, int8_t *kept,
+                                    uint8_t *kept_scales, void *out, hipStream_t stream);
+hipError_t launch_expert_dgrad_kept8(const ExpertRows &r, const void *dy, const void *w,
+                                     int32_t width, int32_t inner, const int8_t *kept,
+                                     const uint8_t *kept_scales, void *act, void *dx,
+                                     hipStream_t stream);
+hipError_t launch_expert_wgrad_kept8(const ExpertRows &r, const void *dy, const int8_t *x,
+                                     const uint8_t *x_scales, int32_t width, int32_t inner,
+                                     bool f32, bool accumulate, void *dw, hipStream_t stream);
+
 }  // namespace epx

@@ -98,6 +98,15 @@ _lib.epx_mxfp4_quantize.argtypes = [_P, ctypes.c_int64, _I32, _P, _P, _P]
 _lib.epx_mxfp4_dequantize.argtypes = [_P, _P, ctypes.c_int64, _I32, _P, _P]
 _lib.epx_expert_gemm_mxfp4.argtypes = [ctypes.POINTER(epx_expert_rows), _P, _P, _P, _P, _I32, _I32, _I32, _I32,
                                        _P, _P, _P]
+_ROWS = ctypes.POINTER(epx_expert_rows)
+for _f in ("epx_int8_quantize", "epx_mxint8_quantize"):
+    getattr(_lib, _f).argtypes = [_P, ctypes.c_int64, _I32, _P, _P, _P]
+for _f in ("epx_int8_dequantize", "epx_mxint8_dequantize"):
+    getattr(_lib, _f).argtypes = [_P, _P, ctypes.c_int64, _I32, _P, _P]
+_lib.epx_expert_gemm_int8.argtypes = [_ROWS, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]
+_lib.epx_expert_gemm_keep8.argtypes = [_ROWS, _P, _P, _I32, _I32, _P, _P, _P, _P]
+_lib.epx_expert_gemm_dgrad_kept8.argtypes = [_ROWS, _P, _P, _I32, _I32, _P, _P, _P, _P, _P]
+_lib.epx_expert_gemm_wgrad_kept8.argtypes = [_ROWS, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P]
 _lib.epx_time_next_call.argtypes = [_P, _P]
 _lib.epx_checked_violations.argtypes = [ctypes.POINTER(ctypes.c_int64), _P]
 _lib.epx_status_string.argtypes = [ctypes.c_int]
@@ -108,7 +117,9 @@ for _f in ("epx_layout_sizes", "epx_get_layout", "epx_dispatch", "epx_combine", 
            "epx_layout_dispatch", "epx_time_next_call", "epx_layout_dispatch_noalloc",
            "epx_checked_violations", "epx_route", "epx_route_backward", "epx_combine_backward",
            "epx_expert_gemm", "epx_expert_gemm_dgrad", "epx_expert_gemm_wgrad", "epx_mxfp4_quantize",
-           "epx_mxfp4_dequantize", "epx_expert_gemm_mxfp4"):
+           "epx_mxfp4_dequantize", "epx_expert_gemm_mxfp4", "epx_int8_quantize", "epx_int8_dequantize",
+           "epx_mxint8_quantize", "epx_mxint8_dequantize", "epx_expert_gemm_int8", "epx_expert_gemm_keep8",
+           "epx_expert_gemm_dgrad_kept8", "epx_expert_gemm_wgrad_kept8"):
     getattr(_lib, _f).restype = ctypes.c_int
 _lib.epx_abi_version.restype = ctypes.c_int32
 NARRAYS = len(LAYOUT_FIELDS)
@@ -643,6 +654,125 @@ def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Ten
                                       FP8_E4M3 if fp8 else BF16, _ptr(out, rtype, "out", (R, width), dev),
                                       _ptr(out_scales, f32, "out_scales", (R, width // 128), dev) if fp8 else None,
                                       _launch_stream(stream, dev)), "epx_expert_gemm_mxfp4")
+
+
+def _rows8_args(values, codes, scales, name, unit):
+    """(rows, inner, addresses, device); rows are the product of all dimensions but the last."""
+    dev = _device(values, name)
+    _need(values, torch.bfloat16, name)
+    if values.dim() < 2:
+        raise ValueError(f"{name}: need at least 2 dimensions")
+    inner, lead = values.shape[-1], tuple(values.shape[:-1])
+    if inner == 0 or inner % unit:
+        raise ValueError(f"{name}: the last dimension must be a multiple of {unit}")
+    ps = (_ptr(scales, torch.uint8, "scales", lead + (inner // 32,), dev) if unit == 32
+          else _ptr(scales, torch.float32, "scales", lead, dev))
+    return values.numel() // inner, inner, values.data_ptr(), _ptr(codes, torch.int8, "codes", lead + (inner,), dev), ps, dev
+
+
+def epx_int8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """bf16 rows [..., inner] to int8 codes [..., inner] and a float32 scale a row [...]."""
+    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 16)
+    _check(_lib.epx_int8_quantize(px, num_rows, inner, pc, ps, _launch_stream(stream, dev)), "epx_int8_quantize")
+
+
+def epx_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """bf16(code * scale) of int8 rows."""
+    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 16)
+    _check(_lib.epx_int8_dequantize(pc, ps, num_rows, inner, po, _launch_stream(stream, dev)), "epx_int8_dequantize")
+
+
+def epx_mxint8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """bf16 rows [..., inner] to int8 codes [..., inner] and a scale byte per 32 values [..., inner/32]."""
+    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 32)
+    _check(_lib.epx_mxint8_quantize(px, num_rows, inner, pc, ps, _launch_stream(stream, dev)), "epx_mxint8_quantize")
+
+
+def epx_mxint8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """The bf16 values that int8 codes and scale bytes stand for (exact)."""
+    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 32)
+    _check(_lib.epx_mxint8_dequantize(pc, ps, num_rows, inner, po, _launch_stream(stream, dev)),
+           "epx_mxint8_dequantize")
+
+
+def _kept_ptrs(codes, scales, name: str, R: int, columns: int, dev: int):
+    """Addresses of [R, columns] activations kept in 8 bits, and of their scale bytes."""
+    if columns % 32:
+        raise ValueError(f"{name}_codes: the last dimension must be a multiple of 32")
+    return (_ptr(codes, torch.int8, name + "_codes", (R, columns), dev),
+            _ptr(scales, torch.uint8, name + "_scales", (R, columns // 32), dev))
+
+
+def epx_expert_gemm_int8(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                         w_scales: torch.Tensor, out: torch.Tensor, act: int = ACT_NONE,
+                         preact_codes: Optional[torch.Tensor] = None, preact_scales: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """epx_expert_gemm for int8 rows (a float32 scale each, as epx_int8_quantize
+    writes them) and int8 weights [n, width or 2 * width, inner] with a scale
+    per column of the product. With ACT_SWIGLU preact_codes and preact_scales, if
+    given, receive the product before the activation in 8 bits."""
+    dev, i8, f32 = _rows_device(rows), torch.int8, torch.float32
+    width, inner, R, n = _columns(out, torch.bfloat16, "out"), _columns(x, i8, "x"), rows.num_rows, rows.num_experts
+    wide = 2 * width if act == ACT_SWIGLU else width
+    pc, ps = None, None
+    if preact_codes is not None or preact_scales is not None:
+        pc, ps = _kept_ptrs(preact_codes, preact_scales, "preact", R, wide, dev)
+    _check(_lib.epx_expert_gemm_int8(ctypes.byref(rows.struct), _ptr(x, i8, "x", (R, inner), dev),
+                                     _ptr(x_scales, f32, "x_scales", (R,), dev),
+                                     _ptr(w, i8, "w", (n, wide, inner), dev),
+                                     _ptr(w_scales, f32, "w_scales", (n, wide), dev), width, inner, act, pc, ps,
+                                     _ptr(out, torch.bfloat16, "out", (R, width), dev), _launch_stream(stream, dev)),
+           "epx_expert_gemm_int8")
+
+
+def epx_expert_gemm_keep8(rows: ExpertRows, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
+                          preact_codes: torch.Tensor, preact_scales: torch.Tensor, stream=None) -> None:
+    """epx_expert_gemm with ACT_SWIGLU that keeps the product before the
+    activation in 8 bits (as epx_mxint8_quantize keeps rows)."""
+    dev, bf16 = _rows_device(rows), torch.bfloat16
+    width, inner, R = _columns(out, bf16, "out"), _columns(x, bf16, "x"), rows.num_rows
+    pc, ps = _kept_ptrs(preact_codes, preact_scales, "preact", R, 2 * width, dev)
+    _check(_lib.epx_expert_gemm_keep8(ctypes.byref(rows.struct), _ptr(x, bf16, "x", (R, inner), dev),
+                                      _ptr(w, bf16, "w", (rows.num_experts, 2 * width, inner), dev), width, inner, pc,
+                                      ps, _ptr(out, bf16, "out", (R, width), dev), _launch_stream(stream, dev)),
+           "epx_expert_gemm_keep8")
+
+
+def epx_expert_gemm_dgrad_kept8(rows: ExpertRows, dy: torch.Tensor, w: torch.Tensor, preact_codes: torch.Tensor,
+                                preact_scales: torch.Tensor, dx: torch.Tensor, act_out: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """epx_expert_gemm_dgrad with input_act=ACT_SWIGLU and pre-activations kept
+    in 8 bits; act_out, if given, receives the activation of the kept values."""
+    dev, bf16 = _rows_device(rows), torch.bfloat16
+    try:
+        n, width, inner = w.shape
+    except (AttributeError, ValueError):
+        _need(w, bf16, "w", 3)
+        raise ValueError("w: need 3 dimensions") from None
+    R = rows.num_rows
+    pc, ps = _kept_ptrs(preact_codes, preact_scales, "preact", R, 2 * inner, dev)
+    _check(_lib.epx_expert_gemm_dgrad_kept8(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev),
+                                            _ptr(w, bf16, "w", (rows.num_experts, width, inner), dev), width, inner, pc,
+                                            ps,
+                                            _ptr(act_out, bf16, "act_out", (R, inner), dev)
+                                            if act_out is not None else None,
+                                            _ptr(dx, bf16, "dx", (R, 2 * inner), dev), _launch_stream(stream, dev)),
+           "epx_expert_gemm_dgrad_kept8")
+
+
+def epx_expert_gemm_wgrad_kept8(rows: ExpertRows, dy: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor,
+                                dw: torch.Tensor, accumulate: bool = False, stream=None) -> None:
+    """epx_expert_gemm_wgrad for rows x kept in 8 bits by epx_mxint8_quantize."""
+    code, dev, bf16 = _logits_dtype(dw, "dw"), _rows_device(rows), torch.bfloat16
+    if dw.dim() != 3:
+        raise ValueError(f"dw: need 3 dimensions, got {tuple(dw.shape)}")
+    n, width, inner = dw.shape
+    R = rows.num_rows
+    pc, ps = _kept_ptrs(x_codes, x_scales, "x", R, inner, dev)
+    _check(_lib.epx_expert_gemm_wgrad_kept8(ctypes.byref(rows.struct), _ptr(dy, bf16, "dy", (R, width), dev), pc, ps,
+                                            width, inner, code, int(bool(accumulate)),
+                                            _ptr(dw, dw.dtype, "dw", (rows.num_experts, width, inner), dev),
+                                            _launch_stream(stream, dev)), "epx_expert_gemm_wgrad_kept8")
 
 
 def relay_capacity(problem: epx_problem) -> int:

@@ -362,7 +362,7 @@ EPX_API epx_status epx_plan_swaps(int32_t num_experts, int32_t num_ranks, int32_
                                   int32_t *rank_load_before, int32_t *rank_load_after,
                                   int32_t *swaps, int32_t *host_bad, void *stream);
 
-/* ---- Buffers of the calls from here to epx_expert_gemm_mxfp4: what a call
+/* ---- Buffers of the calls from here to epx_expert_gemm_wgrad_kept8: what a call
  * writes must not overlap anything else that it is given. An output that
  * starts where another buffer does is refused (EPX_ERR_ARG); other overlaps
  * are not looked for. ---- */
@@ -529,6 +529,95 @@ EPX_API epx_status epx_expert_gemm_mxfp4(const epx_expert_rows *rows, const uint
                                          const uint8_t *w_scales, int32_t width, int32_t inner,
                                          int32_t act, int32_t out_dtype, void *out,
                                          float *out_scales, void *stream);
+
+/* ---- 8-bit rows. Two forms, each with its conversions; num_rows < 2^31,
+ * inner at most 2^20; x, out and codes are 16-byte aligned.
+ * Errors: EPX_ERR_ARG.
+ *
+ * int8 rows: a float32 scale per row (a token, or an output channel of a
+ * weight). scale = max |v| / 127 in float32, at least 2^-125, and 0 for a row
+ * of zeros; code = v / scale, the exact quotient, rounded to nearest (ties to
+ * even), so at most 127 in magnitude. A row that holds an infinity or NaN has
+ * scale NaN and codes 0. Back: bf16(code * scale), rounded once; scales and
+ * codes of any origin serve.
+ *  x       bf16 [num_rows, inner], inner a multiple of 16
+ *  codes   int8 [num_rows, inner]
+ *  scales  float32 [num_rows] */
+EPX_API epx_status epx_int8_quantize(const void *x, int64_t num_rows, int32_t inner, int8_t *codes,
+                                     float *scales, void *stream);
+EPX_API epx_status epx_int8_dequantize(const int8_t *codes, const float *scales, int64_t num_rows,
+                                       int32_t inner, void *out, void *stream);
+
+/* Blocks of 32 under a power of two (OCP Microscaling Formats: MXINT8), for
+ * activations that are kept for the backward pass: 32 consecutive values of a
+ * row share one scale byte b, and a value is code * 2^(b - 127 - 6). Every
+ * such value is a bf16 number, so what is kept is used without a further
+ * rounding. Quantisation: b - 127 = floor(log2(max |v|)), at least -127; code =
+ * v / 2^(b - 133) rounded to nearest even, saturated at 127. A block of zeros
+ * has scale byte 0; one that holds an infinity or NaN has scale byte 255 and
+ * codes 0, and reads as NaN. A code of -128 is never written, and read as what
+ * it is. Dequantisation is exact.
+ *  x       bf16 [num_rows, inner], inner a multiple of 32
+ *  codes   int8 [num_rows, inner]
+ *  scales  uint8 [num_rows, inner / 32] */
+EPX_API epx_status epx_mxint8_quantize(const void *x, int64_t num_rows, int32_t inner,
+                                       int8_t *codes, uint8_t *scales, void *stream);
+EPX_API epx_status epx_mxint8_dequantize(const int8_t *codes, const uint8_t *scales,
+                                         int64_t num_rows, int32_t inner, void *out, void *stream);
+
+/* epx_expert_gemm for int8 rows and int8 weights, as epx_int8_quantize writes
+ * them:
+ *  x         int8 [num_rows, inner], x_scales float32 [num_rows]
+ *  w         int8 [num_experts, width or 2 * width, inner], w_scales float32
+ *            [num_experts, width or 2 * width]
+ *  preact_*  NULL, or with EPX_ACT_SWIGLU int8 [num_rows, 2 * width] and uint8
+ *            [num_rows, 2 * width / 32]: the product before the activation,
+ *            kept as epx_mxint8_quantize keeps rows (from its float32 values);
+ *            width is a multiple of 32 then
+ *  out       bf16 [num_rows, width]
+ * A product is the sum over inner, exact in 32 bits, rounded to float32, times
+ * the row's scale, times the column's (each rounded to float32); then the
+ * activation and the rounding to bf16 of epx_expert_gemm. inner is a multiple
+ * of 16 of at most 2^17 - 16, width of 8; rows of one expert's matrix times
+ * inner at most 2^30; x, w, w_scales, out and preact_codes are 16-byte
+ * aligned, x_scales to 4 bytes. Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_int8(const epx_expert_rows *rows, const int8_t *x,
+                                        const float *x_scales, const int8_t *w,
+                                        const float *w_scales, int32_t width, int32_t inner,
+                                        int32_t act, int8_t *preact_codes, uint8_t *preact_scales,
+                                        void *out, void *stream);
+
+/* epx_expert_gemm with EPX_ACT_SWIGLU that keeps the product before the
+ * activation in 8 bits in place of bf16: preact_codes int8 [num_rows, 2 *
+ * width] and preact_scales uint8 [num_rows, 2 * width / 32], quantised from
+ * the float32 sums as epx_mxint8_quantize does. out is that of
+ * epx_expert_gemm. width is a multiple of 32, else sizes and alignment as
+ * there; preact_codes is 16-byte aligned. Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_keep8(const epx_expert_rows *rows, const void *x, const void *w,
+                                         int32_t width, int32_t inner, int8_t *preact_codes,
+                                         uint8_t *preact_scales, void *out, void *stream);
+
+/* epx_expert_gemm_dgrad with input_act EPX_ACT_SWIGLU and pre-activations kept
+ * in 8 bits: preact_codes int8 [num_rows, 2 * inner], preact_scales uint8
+ * [num_rows, 2 * inner / 32].
+ *  act_out  NULL, or bf16 [num_rows, inner]: silu(gate) * up of the kept
+ *           values, the product's input again, for the weights' gradient
+ * inner is a multiple of 32; act_out and preact_codes are 16-byte aligned.
+ * Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_dgrad_kept8(const epx_expert_rows *rows, const void *dy,
+                                               const void *w, int32_t width, int32_t inner,
+                                               const int8_t *preact_codes,
+                                               const uint8_t *preact_scales, void *act_out,
+                                               void *dx, void *stream);
+
+/* epx_expert_gemm_wgrad for rows x kept in 8 bits: x_codes int8 [num_rows,
+ * inner], x_scales uint8 [num_rows, inner / 32], as epx_mxint8_quantize
+ * writes them. dw is that of epx_expert_gemm_wgrad on the values kept. inner is
+ * a multiple of 32. Errors: EPX_ERR_ARG. */
+EPX_API epx_status epx_expert_gemm_wgrad_kept8(const epx_expert_rows *rows, const void *dy,
+                                               const int8_t *x_codes, const uint8_t *x_scales,
+                                               int32_t width, int32_t inner, int32_t dw_dtype,
+                                               int32_t accumulate, void *dw, void *stream);
 
 /* Synchronises `stream`, then reads totals[3]: EPX_OK, or EPX_ERR_INDEX when
  * the last layout on this layout's arrays saw out-of-range expert ids (their
