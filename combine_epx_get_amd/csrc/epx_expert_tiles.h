@@ -257,6 +257,9 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
             // 1662 with two buffers of each and all copies in one half; five
             // buffers of 32 of the sum 2044).
             static_assert(S == 2 && BK == 64, "");
+            // int8: arithmetic may move between the rounds (32768 ragged rows, 16
+            // experts, 2 x 2048 x 7168: 800 us against 815; bf16 gains nothing)
+            constexpr int kMayCross = kI8 ? 0x6 : 0;
             constexpr int kReads = NI + NJ;
             // reads and copies before each of the NI rounds of NJ instructions
             // (transposing reads are twice as many, and spread further)
@@ -303,7 +306,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
                         mfma_in_place(acc[i][j], pf[0][i], qf[0][j]);
-                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(kMayCross);
                 }
                 wait_copies<kPCopies>();   // all but the ones just made
 #pragma unroll
@@ -321,7 +324,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                         else
                             mfma_in_place(acc[i][j], pf[1][i], qf[1][j]);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(kMayCross);
                 }
                 const uint32_t free_p = p0, free_q = q0;
                 p0 = p1;

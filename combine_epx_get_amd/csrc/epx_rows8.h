@@ -47,17 +47,15 @@ __device__ __forceinline__ u32x2 mxint8_codes(const float (&v)[8], uint32_t b)
     return b == 255 ? u32x2{0, 0} : o;
 }
 
-// 8 codes times their step, as bf16: the products are bf16 numbers, so their
+// 4 codes times their step, as bf16: the products are bf16 numbers, so their
 // upper halves are all there is.
-__device__ __forceinline__ u32x4 mxint8_bf16(u32x2 c, float step)
+__device__ __forceinline__ u32x2 mxint8_bf16(uint32_t c, float step)
 {
-    u32x4 w;
+    u32x2 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t half = i < 2 ? c.x : c.y;
-        w[i] = __builtin_amdgcn_perm(__float_as_uint(signed_byte(half, i % 2 * 2 + 1) * step),
-                                     __float_as_uint(signed_byte(half, i % 2 * 2) * step), 0x07060302u);
-    }
+    for (int i = 0; i < 2; ++i)
+        w[i] = __builtin_amdgcn_perm(__float_as_uint(signed_byte(c, 2 * i + 1) * step),
+                                     __float_as_uint(signed_byte(c, 2 * i) * step), 0x07060302u);
     return w;
 }
 

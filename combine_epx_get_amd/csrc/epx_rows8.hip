@@ -222,7 +222,9 @@ __global__ __launch_bounds__(kThreads) void mxint8_dequantize_kernel(const u32x2
         const int64_t i = base + u * kThreads;
         if (i >= nvec)
             return;
-        __builtin_nontemporal_store(mxint8_bf16(cs[u], mxint8_step(bs[u])), out + i);
+        const float step = mxint8_step(bs[u]);
+        const u32x2 lo = mxint8_bf16(cs[u].x, step), hi = mxint8_bf16(cs[u].y, step);
+        __builtin_nontemporal_store(u32x4{lo.x, lo.y, hi.x, hi.y}, out + i);
     }
 }
 
