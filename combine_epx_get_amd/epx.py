@@ -656,8 +656,20 @@ def epx_expert_gemm_mxfp4(rows: ExpertRows, x: torch.Tensor, x_scales: torch.Ten
                                       _launch_stream(stream, dev)), "epx_expert_gemm_mxfp4")
 
 
-def _rows8_args(values, codes, scales, name, unit):
+def _rows8_args(values, codes, scales, name, unit, scale_dtype):
     """(rows, inner, addresses, device); rows are the product of all dimensions but the last."""
+    try:
+        shape, dev = values.shape, values.get_device()
+        lead, inner = shape[:-1], shape[-1]
+        # the usual call, in as few steps as tell it (these calls are short)
+        if (len(shape) > 1 and inner and inner % unit == 0 and values.dtype is torch.bfloat16
+                and codes.dtype is torch.int8 and scales.dtype is scale_dtype and codes.shape == shape
+                and scales.shape == (lead if unit == 16 else lead + (inner // 32,))
+                and dev >= 0 and dev == codes.get_device() == scales.get_device() == _current_device()
+                and values.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()):
+            return values.numel() // inner, inner, values.data_ptr(), codes.data_ptr(), scales.data_ptr(), dev
+    except (AttributeError, IndexError):   # no tensor, or one without dimensions
+        pass
     dev = _device(values, name)
     _need(values, torch.bfloat16, name)
     if values.dim() < 2:
@@ -665,32 +677,32 @@ def _rows8_args(values, codes, scales, name, unit):
     inner, lead = values.shape[-1], tuple(values.shape[:-1])
     if inner == 0 or inner % unit:
         raise ValueError(f"{name}: the last dimension must be a multiple of {unit}")
-    ps = (_ptr(scales, torch.uint8, "scales", lead + (inner // 32,), dev) if unit == 32
-          else _ptr(scales, torch.float32, "scales", lead, dev))
-    return values.numel() // inner, inner, values.data_ptr(), _ptr(codes, torch.int8, "codes", lead + (inner,), dev), ps, dev
+    _ptr(codes, torch.int8, "codes", lead + (inner,), dev)
+    _ptr(scales, scale_dtype, "scales", lead if unit == 16 else lead + (inner // 32,), dev)
+    raise ValueError(f"{name}: not a plain tensor")
 
 
 def epx_int8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """bf16 rows [..., inner] to int8 codes [..., inner] and a float32 scale a row [...]."""
-    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 16)
+    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 16, torch.float32)
     _check(_lib.epx_int8_quantize(px, num_rows, inner, pc, ps, _launch_stream(stream, dev)), "epx_int8_quantize")
 
 
 def epx_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """bf16(code * scale) of int8 rows."""
-    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 16)
+    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 16, torch.float32)
     _check(_lib.epx_int8_dequantize(pc, ps, num_rows, inner, po, _launch_stream(stream, dev)), "epx_int8_dequantize")
 
 
 def epx_mxint8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """bf16 rows [..., inner] to int8 codes [..., inner] and a scale byte per 32 values [..., inner/32]."""
-    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 32)
+    num_rows, inner, px, pc, ps, dev = _rows8_args(x, codes, scales, "x", 32, torch.uint8)
     _check(_lib.epx_mxint8_quantize(px, num_rows, inner, pc, ps, _launch_stream(stream, dev)), "epx_mxint8_quantize")
 
 
 def epx_mxint8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """The bf16 values that int8 codes and scale bytes stand for (exact)."""
-    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 32)
+    num_rows, inner, po, pc, ps, dev = _rows8_args(out, codes, scales, "out", 32, torch.uint8)
     _check(_lib.epx_mxint8_dequantize(pc, ps, num_rows, inner, po, _launch_stream(stream, dev)),
            "epx_mxint8_dequantize")
 
