@@ -413,22 +413,29 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
             a.kept_scales[(row * 2 + ups) * (a.np / 32) + c / 32] = (uint8_t)b;
     }
 
-    template <int N> static __device__ __forceinline__ Cols<N> kept(const Args8 &a, int64_t row, int c, bool ups)
-    {
-        static_assert(N == 8, "");
-        Cols<8> o;
-        u32x2 v = {0, 0};
-        uint32_t b = 127;
-        if (c < a.np) {
-            v = *(const u32x2 *)(a.kept + (row * 2 + ups) * a.np + c);
-            b = a.kept_scales[(row * 2 + ups) * (a.np / 32) + c / 32];
-        }
-        const float step = mxint8_step(b);
+    // Gates and ups [c, c + 8) of a row as they were kept.
+    struct KeptPair {
+        u32x2 code[2];
+        uint32_t scale[2];
+        // (codes and scale bytes of the tile's rows; past its rows zeros come)
+        __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, int np, int r, int c)
+        {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            o.v[q] = signed_byte(q < 4 ? v.x : v.y, q % 4) * step;
-        return o;
-    }
+            for (int h = 0; h < 2; ++h) {
+                code[h] = __builtin_amdgcn_raw_buffer_load_b64(codes, (2 * r + h) * np + c, 0, 0);
+                scale[h] = __builtin_amdgcn_raw_buffer_load_b8(scales, (2 * r + h) * (np / 32) + c / 32, 0, 0);
+            }
+        }
+        __device__ __forceinline__ Cols<8> values(int h) const
+        {
+            Cols<8> o;
+            const float step = mxint8_step(scale[h]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                o.v[q] = signed_byte(q < 4 ? code[h].x : code[h].y, q % 4) * step;
+            return o;
+        }
+    };
 
     // Results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
     // columns 4 g .. 4 g + 3 of fragment i. Two fragments are neighbours
@@ -443,12 +450,45 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
         const int col0 = t.p * PC;
         constexpr bool kMerge = kPCols && OP != kWgradF32 && NI % 2 == 0;
         constexpr int W = kMerge ? 2 : GI, NG = kHalf / W;
-        if constexpr (kMerge) {
+        if constexpr (kMerge && OP != kDgradKept) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
                     merge_columns(acc[2 * n][j], acc[2 * n + 1][j]);
+        }
+        // What the rows need from memory is loaded some rows ahead of its use (all
+        // of it before the first row is written, for the scales of int8 rows): the
+        // compiler moves no load over a store, so that each would wait for its own
+        // (input gradient of 32768 rows, 16 experts of 7168 x 2048: 895 against 907
+        // us). By 32-bit offsets: 64-bit addresses of rows ahead took 70 registers
+        // to memory, and 950 us.
+        constexpr int kAhead = OP == kDgradKept ? (N * NG < 8 ? N * NG : 8) : 1;
+        [[maybe_unused]] KeptPair pairs[kAhead];
+        [[maybe_unused]] __amdgpu_buffer_rsrc_t kept_codes, kept_scales;
+        if constexpr (OP == kDgradKept) {
+            const uint32_t bytes = (uint32_t)min(t.rows, TQ) * 2u * (uint32_t)a.np;
+            kept_codes = read_buffer((const char *)a.kept + (int64_t)t.row0 * 2 * a.np, bytes);
+            kept_scales = read_buffer((const char *)a.kept_scales + (int64_t)t.row0 * 2 * (a.np / 32), bytes / 32);
+        }
+        [[maybe_unused]] auto load_pair = [&](int x) {
+            if constexpr (OP == kDgradKept)
+                pairs[x % kAhead].load(kept_codes, kept_scales, a.np, wq * (TQ / WQ) + (j0 + x / NG) * 16 + m,
+                                       col0 + wp * (PC / WP) + x % NG * 32 + 8 * g);
+        };
+        if constexpr (OP == kDgradKept) {
+            static_assert(W == 2, "");
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x)
+                load_pair(x);
+        }
+        [[maybe_unused]] float srow[kI8 ? N : 1];
+        if constexpr (kI8) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int r = wq * (TQ / WQ) + (j0 + j) * 16 + m;
+                srow[j] = r < t.rows ? a.q_scales[(int64_t)t.row0 + r] : 0.0f;
+            }
         }
         // int8: the scales of this lane's columns of w
         [[maybe_unused]] Cols<4 * W> su[NG], sv[NG];
@@ -465,13 +505,13 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int r = wq * (TQ / WQ) + (j0 + j) * 16 + m;
-            [[maybe_unused]] float sr = 0.0f;
-            if constexpr (kI8)
-                sr = r < t.rows ? a.q_scales[(int64_t)t.row0 + r] : 0.0f;
+            [[maybe_unused]] const float sr = kI8 ? srow[kI8 ? j : 0] : 0.0f;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const int c = col0 + wp * (PC / WP) + n * 16 * W + 4 * W * g;
                 Cols<4 * W> u, v;
+                if constexpr (kMerge && OP == kDgradKept)   // (here: fewer registers beside what is ahead)
+                    merge_columns(acc[2 * n][j], acc[2 * n + 1][j]);
 #pragma unroll
                 for (int i = 0; i < W; ++i)
 #pragma unroll
@@ -517,8 +557,10 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                     if constexpr (OP == kDgradGlu || OP == kDgradKept) {
                         Cols<4 * W> gate, up;
                         if constexpr (OP == kDgradKept) {
-                            gate = kept<4 * W>(a, row, c, false);
-                            up = kept<4 * W>(a, row, c, true);
+                            gate = pairs[(j * NG + n) % kAhead].values(0);
+                            up = pairs[(j * NG + n) % kAhead].values(1);
+                            if (j * NG + n + kAhead < N * NG)
+                                load_pair(j * NG + n + kAhead);
                         } else {
                             const uint16_t *pre = a.preact_in + row * 2 * a.np;
                             gate = load_bf16<4 * W>(pre, c, a.np);

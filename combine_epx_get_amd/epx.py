@@ -677,9 +677,8 @@ def _rows8_args(values, codes, scales, name, unit, scale_dtype):
     inner, lead = values.shape[-1], tuple(values.shape[:-1])
     if inner == 0 or inner % unit:
         raise ValueError(f"{name}: the last dimension must be a multiple of {unit}")
-    _ptr(codes, torch.int8, "codes", lead + (inner,), dev)
-    _ptr(scales, scale_dtype, "scales", lead if unit == 16 else lead + (inner // 32,), dev)
-    raise ValueError(f"{name}: not a plain tensor")
+    return (values.numel() // inner, inner, values.data_ptr(), _ptr(codes, torch.int8, "codes", lead + (inner,), dev),
+            _ptr(scales, scale_dtype, "scales", lead if unit == 16 else lead + (inner // 32,), dev), dev)
 
 
 def epx_int8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
