@@ -18,10 +18,6 @@
 namespace epx {
 namespace {
 
-struct KeptArgs : Args {
-    const uint8_t *scales;   // of P, a byte per 32 columns
-};
-
 // A step of x on its way to LDS: BK rows of TP columns, spread over LANES lanes.
 // A lane has kUnits units of 16 columns, each a load of codes and one of their
 // scale byte; all of its units have the same columns.
@@ -78,7 +74,7 @@ template <int TP, int BK, int LANES> struct Stage {
 // took longer at every size: what bounds these tiles is the instructions of the
 // conversion, not the memory's latency.)
 template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK> struct KeptKernel {
-    using Base = Kernel<F32 ? kWgradF32 : kWgrad, TP, TQ, BK, 2, WP, WQ, WK>;
+    using Base = Kernel<F32 ? kWgradKeptF32 : kWgradKept, TP, TQ, BK, 2, WP, WQ, WK>;
     static constexpr int kWaves = WP * WQ, kLanes = kWaves * kWave;
     static constexpr int NI = Base::NI, NJ = Base::NJ;
     static constexpr int kPBytes = Base::kPBytes, kQBytes = Base::kQBytes, kQCopies = Base::kQCopies;
@@ -92,14 +88,14 @@ template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK> struct KeptK
     static constexpr int kPerSimd = kByLds < 2 ? 2 : kByLds > 4 ? 4 : kByLds;
     static_assert(kLds <= 160 * 1024, "");
 
-    static __device__ __forceinline__ void run(const KeptArgs &a, const Tile &t, char *smem)
+    static __device__ __forceinline__ void run(const Args8 &a, const Tile &t, char *smem)
     {
         const int of_all = uniform(threadIdx.x >> 6), group = of_all / kWaves;
         const int wave = of_all % kWaves, wp = wave % WP, wq = wave / WP;
         const int steps = (t.sum + BK - 1) / BK, own_steps = (steps + WK - 1) / WK;
         const int col0 = t.p * TP, np32 = a.np / 32;
         const char *pb = uniform_ptr(a.p + (int64_t)t.row0 * a.np + col0);
-        const char *sb = uniform_ptr(a.scales + (int64_t)t.row0 * np32 + col0 / 32);
+        const char *sb = uniform_ptr(a.kept_scales + (int64_t)t.row0 * np32 + col0 / 32);
         const char *qb = uniform_ptr(a.q + ((int64_t)t.row0 * a.nq + t.q * TQ) * 2);
         uint32_t q_off[kQCopies];
         Base::template copy_offsets<true, TQ, kQCopies, 2, false>(wave, 0, a.nq, 0, q_off);
@@ -194,7 +190,7 @@ template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK> struct KeptK
 // the bf16 kernel holds them, would leave no registers for the codes.)
 template <bool F32> struct KeptDeep {
     static constexpr int TP = 256, TQ = 256, BK = 64, WP = 4, WQ = 2;
-    using Base = Kernel<F32 ? kWgradF32 : kWgrad, TP, TQ, BK, 2, WP, WQ>;
+    using Base = Kernel<F32 ? kWgradKeptF32 : kWgradKept, TP, TQ, BK, 2, WP, WQ>;
     static constexpr int NI = Base::NI, NJ = Base::NJ;
     static constexpr int kPBytes = Base::kPBytes, kQBytes = Base::kQBytes, kQCopies = Base::kQCopies;
     static constexpr int kLds = 2 * kPBytes + 3 * kQBytes;
@@ -205,13 +201,13 @@ template <bool F32> struct KeptDeep {
     static constexpr int kMayCross = 0x6;
     static_assert(NI == 4 && NJ == 8 && X::kUnits == 2 && kQCopies == 4, "");
 
-    static __device__ __forceinline__ void run(const KeptArgs &a, const Tile &t, char *smem)
+    static __device__ __forceinline__ void run(const Args8 &a, const Tile &t, char *smem)
     {
         const int wave = uniform(threadIdx.x >> 6), wp = wave % WP, wq = wave / WP;
         const int steps = (t.sum + BK - 1) / BK;
         const int col0 = t.p * TP, np32 = a.np / 32;
         const char *pb = uniform_ptr(a.p + (int64_t)t.row0 * a.np + col0);
-        const char *sb = uniform_ptr(a.scales + (int64_t)t.row0 * np32 + col0 / 32);
+        const char *sb = uniform_ptr(a.kept_scales + (int64_t)t.row0 * np32 + col0 / 32);
         const char *qb = uniform_ptr(a.q + ((int64_t)t.row0 * a.nq + t.q * TQ) * 2);
         uint32_t q_off[kQCopies];
         Base::template copy_offsets<true, TQ, kQCopies, 2, false>(wave, 0, a.nq, 0, q_off);
@@ -316,7 +312,7 @@ template <bool F32> struct KeptDeep {
     }
 };
 
-template <bool F32> __global__ __launch_bounds__(512, 2) void wgrad_kept_deep_kernel(KeptArgs a)
+template <bool F32> __global__ __launch_bounds__(512, 2) void wgrad_kept_deep_kernel(Args8 a)
 {
     using K = KeptDeep<F32>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
@@ -327,7 +323,7 @@ template <bool F32> __global__ __launch_bounds__(512, 2) void wgrad_kept_deep_ke
 
 template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK>
 __global__ __launch_bounds__(WP *WQ *WK *kWave, (KeptKernel<F32, TP, TQ, BK, WP, WQ, WK>::kPerSimd))
-void wgrad_kept_kernel(KeptArgs a)
+void wgrad_kept_kernel(Args8 a)
 {
     using K = KeptKernel<F32, TP, TQ, BK, WP, WQ, WK>;
     __shared__ __attribute__((aligned(1024))) char smem[K::kLds];
@@ -337,7 +333,7 @@ void wgrad_kept_kernel(KeptArgs a)
 }
 
 template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK = 1>
-hipError_t start_kept(KeptArgs a, hipStream_t stream)
+hipError_t start_kept(Args8 a, hipStream_t stream)
 {
     a.pt = (a.np + TP - 1) / TP;
     a.qt = (a.nq + TQ - 1) / TQ;
@@ -349,7 +345,7 @@ hipError_t start_kept(KeptArgs a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <bool F32> hipError_t start_kept_deep(KeptArgs a, hipStream_t stream)
+template <bool F32> hipError_t start_kept_deep(Args8 a, hipStream_t stream)
 {
     a.pt = (a.np + 255) / 256;
     a.qt = (a.nq + 255) / 256;
@@ -374,7 +370,7 @@ template <bool F32> hipError_t start_kept_deep(KeptArgs a, hipStream_t stream)
 // 11.0 / 15.7; 2 of 1408 x 2912, 647 rows 30 / 24 / 28; 16 of 2048 x 7168, 64 rows
 // 362 / 159 / 174, 256 rows 464 / 265 / 258, 1024 rows 973 / 648 / 526; 64 of 1024 x
 // 2048, 64 rows 202 / 77 / 100; 1 of 4096 x 4096, 2048 rows 117 / 85 / 66.
-template <bool F32> hipError_t start_wgrad_kept(const KeptArgs &a, hipStream_t stream)
+template <bool F32> hipError_t start_wgrad_kept(const Args8 &a, hipStream_t stream)
 {
     const auto tiles = [&](int p, int q) {
         return (int64_t)((a.np + p - 1) / p) * ((a.nq + q - 1) / q) * a.r.n;
@@ -436,7 +432,7 @@ hipError_t launch_expert_wgrad_kept8(const ExpertRows &r, const void *dy, const 
                                      const uint8_t *x_scales, int32_t width, int32_t inner,
                                      bool f32, bool accumulate, void *dw, hipStream_t stream)
 {
-    KeptArgs a = {};
+    Args8 a = {};
     a.r = r;
     a.p = (const char *)x;
     a.q = (const char *)dy;
@@ -444,7 +440,7 @@ hipError_t launch_expert_wgrad_kept8(const ExpertRows &r, const void *dy, const 
     a.nq = width;
     a.out = dw;
     a.accumulate = accumulate;
-    a.scales = x_scales;
+    a.kept_scales = const_cast<uint8_t *>(x_scales);
     return f32 ? start_wgrad_kept<true>(a, stream) : start_wgrad_kept<false>(a, stream);
 }
 

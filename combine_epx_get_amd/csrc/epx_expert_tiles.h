@@ -11,15 +11,17 @@ namespace {
 
 // Keep: the pre-activations are written in 8 bits (MXINT8). Int8: operands in
 // int8 with a scale per row of x and of w. Kept: the input's activation is
-// taken from pre-activations kept in 8 bits.
+// taken from pre-activations kept in 8 bits; for the weight gradient, the rows
+// summed over are.
 enum Op {
     kForward, kForwardGlu, kDgrad, kDgradGlu, kWgrad, kWgradF32,
-    kForwardKeep, kInt8, kInt8Glu, kInt8Keep, kDgradKept
+    kForwardKeep, kInt8, kInt8Glu, kInt8Keep, kDgradKept, kWgradKept, kWgradKeptF32
 };
 constexpr bool is_int8(int op) { return op == kInt8 || op == kInt8Glu || op == kInt8Keep; }
 constexpr bool is_keep(int op) { return op == kForwardKeep || op == kInt8Keep; }
 constexpr bool is_glu(int op) { return op == kForwardGlu || op == kInt8Glu || is_keep(op); }
-constexpr bool is_weights(int op) { return op == kWgrad || op == kWgradF32; }
+constexpr bool is_f32(int op) { return op == kWgradF32 || op == kWgradKeptF32; }
+constexpr bool is_weights(int op) { return op == kWgrad || op == kWgradKept || is_f32(op); }
 constexpr bool is_gradient(int op) { return op == kDgrad || op == kDgradGlu || op == kDgradKept || is_weights(op); }
 
 struct Args {
@@ -400,12 +402,12 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
     // bits. The four lanes of a row hold a block of 32 (np is a multiple of 32).
     static __device__ __forceinline__ void keep(const Args8 &a, int64_t row, int c, const Cols<8> &o, bool ups)
     {
-        uint32_t most = 0;
+        // (a maximum that hands on a NaN)
+        float most = fabsf(o.v[0]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            most = max(most, __float_as_uint(o.v[q]) & 0x7FFFFFFFu);
-        most = max_of_four(most);
-        const uint32_t b = most >> 23;
+        for (int q = 1; q < 8; ++q)
+            most = __builtin_elementwise_maximum(most, fabsf(o.v[q]));
+        const uint32_t b = max_of_four(__float_as_uint(most) & 0x7FFFFFFFu) >> 23;
         if (c >= a.np)
             return;
         *(u32x2 *)(a.kept + (row * 2 + ups) * a.np + c) = mxint8_codes(o.v, b);
@@ -437,6 +439,15 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
         }
     };
 
+    template <int N>
+    static __device__ __forceinline__ void store(uint16_t *row, int c, int width, const Cols<N> &o)
+    {
+        if constexpr (OP >= kForwardKeep)
+            store_bf16_hw(row, c, width, o);
+        else
+            store_bf16(row, c, width, o);
+    }
+
     // Results: lane (m, g) of fragment pair (i, j) has row j * 16 + m and
     // columns 4 g .. 4 g + 3 of fragment i. Two fragments are neighbours
     // already where P's rows are read that way (GI), and are merged here
@@ -448,7 +459,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
         const int m = lane_id() & 15, g = lane_id() >> 4;
         constexpr int PC = kGlu ? TP / 2 : TP;
         const int col0 = t.p * PC;
-        constexpr bool kMerge = kPCols && OP != kWgradF32 && NI % 2 == 0;
+        constexpr bool kMerge = kPCols && !is_f32(OP) && NI % 2 == 0;
         constexpr int W = kMerge ? 2 : GI, NG = kHalf / W;
         if constexpr (kMerge && OP != kDgradKept) {
 #pragma unroll
@@ -531,10 +542,10 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                     if (row >= a.nq)
                         continue;
                     const int64_t o = ((int64_t)t.expert * a.nq + row) * a.np;
-                    if constexpr (OP == kWgradF32)
+                    if constexpr (is_f32(OP))
                         store_f32((float *)a.out + o, c, a.np, u, a.accumulate);
                     else
-                        store_bf16((uint16_t *)a.out + o, c, a.np, u);
+                        store((uint16_t *)a.out + o, c, a.np, u);
                 } else {
                     if (r >= t.rows)
                         continue;
@@ -556,6 +567,7 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                     }
                     if constexpr (OP == kDgradGlu || OP == kDgradKept) {
                         Cols<4 * W> gate, up;
+                        [[maybe_unused]] Cols<4 * W> act;
                         if constexpr (OP == kDgradKept) {
                             gate = pairs[(j * NG + n) % kAhead].values(0);
                             up = pairs[(j * NG + n) % kAhead].values(1);
@@ -566,26 +578,23 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
                             gate = load_bf16<4 * W>(pre, c, a.np);
                             up = load_bf16<4 * W>(pre + a.np, c, a.np);
                         }
-                        if constexpr (OP == kDgradKept) {
-                            if (a.act) {
-                                Cols<4 * W> o;
-#pragma unroll
-                                for (int q = 0; q < 4 * W; ++q)
-                                    o.v[q] = swiglu(gate.v[q], up.v[q]);
-                                store_bf16(a.act + row * a.np, c, a.np, o);
-                            }
-                        }
 #pragma unroll
                         for (int q = 0; q < 4 * W; ++q) {
                             const float s = sigmoid32(gate.v[q]), d = u.v[q];
                             u.v[q] = d * up.v[q] * (s * (1.0f + gate.v[q] * (1.0f - s)));
                             v.v[q] = d * (gate.v[q] * s);
+                            if constexpr (OP == kDgradKept)
+                                act.v[q] = gate.v[q] * s * up.v[q];
                         }
                         uint16_t *dx = (uint16_t *)a.out + row * 2 * a.np;
-                        store_bf16(dx, c, a.np, u);
-                        store_bf16(dx + a.np, c, a.np, v);
+                        store(dx, c, a.np, u);
+                        store(dx + a.np, c, a.np, v);
+                        if constexpr (OP == kDgradKept) {
+                            if (a.act)
+                                store(a.act + row * a.np, c, a.np, act);
+                        }
                     } else {
-                        store_bf16((uint16_t *)a.out + row * a.np, c, a.np, u);
+                        store((uint16_t *)a.out + row * a.np, c, a.np, u);
                     }
                 }
             }
@@ -708,15 +717,40 @@ bool start_split(const A &a, int64_t rows, hipStream_t stream, hipError_t &statu
 // the input, 1 of 3000, 7168 x 512 (188) 42.7 / 51.8; 16 of 96, 2048 x 1024
 // (256) 17.3 / 18.8; but 8 of 300, 1000 x 1000 (328) 22.3 / 18.3.
 enum TileSize { kLarge, kSquare, kSmall, kSmallSplit };
-TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, int64_t sum)
+// A round's time for each, ns: a start and its growth with the sum (in 80ths).
+struct TileCosts {
+    int64_t large, large_sum, square, square_sum, small, small_sum, small_slots;
+};
+constexpr TileCosts kCosts = {9000, 1880, 4500, 1320, 4200, 1008, 512};
+// Forms in 8 bits, whose small tiles have two buffers for sums up to 1280 (of
+// bf16 values, or of pairs of int8), three a CU: one writes while others
+// multiply. us, large / square / small with three buffers / with two. Forward,
+// kept, gated: 16 experts of 2048 rows, 2048 x 64 110 / 107 / 139 / 106, x 256
+// 140 / 144 / 196 / 152, x 512 204 / 245 / 300 / 283; 4 of 1000, 1088 x 256 18.0 /
+// 17.7 / 19.1 / 15.9; 2 of 8000, 640 x 320 35 / 28.7 / 36 / 30.6; 37 of 92, 992 x 88
+// 15.6 / 13.8 / 15.2 / 12.2; 24 of 83, 544 x 1048 20.9 / 20.4 / 20.3 / 18.7. int8: 16
+// of 2048, 2048 x 64 84 / 85 / 132 / 97, x 512 115 / 122 / 176 / 141, x 2048 270 /
+// 332 / 414 / 405; 13 of 461, 1280 x 240 13.7 / 13.9 / 14.7 / 12.3; 2 of 1337, 1408 x
+// 6512 75 / 70 / 98 / 103; 16 of 96, 2048 x 7168 95 / 100 / 125 / 137.
+constexpr TileCosts kCosts8 = {9500, 1520, 4800, 1040, 3900, 1000, 768};
+// The gradient through kept pre-activations, which writes both gradients and
+// the activation, from codes, at about 170 cycles a result of a wave. As above:
+// 16 experts of 2048 rows, 64 x 2048 185 / 173 / 186 / 162, 256 x 2048 192 / 216 /
+// 219 / 200, 512 x 2048 221 / 257 / 257 / 246, 1024 x 2048 271 / 327 / 350 / 331; 1 of
+// 4632, 192 x 1088 30.9 / 19.7 / 18.1 / 16.5; 4 of 1000, 512 x 1088 36 / 23.6 / 23.0
+// / 20.5; 2 of 8000, 320 x 640 35 / 31.6 / 31.0 / 27.8; 37 of 92, 88 x 992 15.9 /
+// 15.9 / 15.6 / 13.5; but 24 of 83, 1048 x 544 24 / 22 / 15.0 / 17.2 (above 512 three).
+constexpr TileCosts kCostsKept = {36000, 1424, 18000, 1440, 13700, 1304, 768};
+
+template <int OP> TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, int64_t sum)
 {
+    constexpr TileCosts c = OP < kForwardKeep ? kCosts : OP == kDgradKept ? kCostsKept : kCosts8;
     auto rounds = [&](int height, int width, int64_t slots) {
         return (tiles_of(r, height, columns, columns_of_256 * width / 256) + slots - 1) / slots;
     };
-    // ns
-    const int64_t large = rounds(256, 256, 256) * (9000 + sum * 47 / 2);
-    const int64_t square = rounds(128, 128, 512) * (4500 + sum * 33 / 2);
-    const int64_t small = rounds(64, 128, 512) * (4200 + sum * 63 / 5);
+    const int64_t large = rounds(256, 256, 256) * (c.large + sum * c.large_sum / 80);
+    const int64_t square = rounds(128, 128, 512) * (c.square + sum * c.square_sum / 80);
+    const int64_t small = rounds(64, 128, c.small_slots) * (c.small + sum * c.small_sum / 80);
     if (large <= square && large <= small)
         return kLarge;
     if (square <= small)
@@ -744,7 +778,7 @@ template <int OP, typename A> hipError_t start_forward(const A &a, hipStream_t s
     if (start_split<OP>(a, rows, stream, status))
         return status;
     if (rows > 64 * n) {
-        const TileSize size = best_tiles(a.r, a.np, is_glu(OP) ? 128 : 256, a.sum);
+        const TileSize size = best_tiles<OP>(a.r, a.np, is_glu(OP) ? 128 : 256, a.sum);
         if (size == kLarge)
             return start<OP, 256, 256, 64, 2, 4, 2>(a, rows, stream);
         if (size == kSquare)
@@ -752,9 +786,17 @@ template <int OP, typename A> hipError_t start_forward(const A &a, hipStream_t s
         if (size == kSmallSplit)
             return start<OP, 128, 64, 64, 3, P, Q, 2>(a, rows, stream);
     }
-    if (rows > 64 * n || (rows > 20 * n && tiles_of(a.r, 64, a.np, is_glu(OP) ? 64 : 128) >= 256))
-        return start<OP, 128, 64, 64, 3, P, Q>(a, rows, stream);
-    return start<OP, 128, 32, 64, 4, P, Q>(a, rows, stream);
+    const bool wide = rows > 64 * n || (rows > 20 * n && tiles_of(a.r, 64, a.np, is_glu(OP) ? 64 : 128) >= 256);
+    if constexpr (OP >= kForwardKeep) {
+        // two buffers as said above; sums of few rows an expert, which wait for
+        // the weights, up to half as long (int8, 64 of 16 rows, 1024 x 2048 42.0 with
+        // three buffers, 45.2 with two; 42 of 20, 416 x 592 6.8 with four, 6.2 with two)
+        if (wide && a.sum <= (rows > 64 * n ? 1280 : 640))
+            return start<OP, 128, 64, 64, 2, P, Q>(a, rows, stream);
+        if (!wide && a.sum <= 640)
+            return start<OP, 128, 32, 64, 2, P, Q>(a, rows, stream);
+    }
+    return wide ? start<OP, 128, 64, 64, 3, P, Q>(a, rows, stream) : start<OP, 128, 32, 64, 4, P, Q>(a, rows, stream);
 }
 
 // The input gradient's. Few rows an expert, us, large / small tiles: 16 experts
@@ -765,13 +807,17 @@ template <int OP, typename A> hipError_t start_dgrad(const A &a, hipStream_t str
     hipError_t status;
     if (start_split<OP>(a, rows, stream, status))
         return status;
-    const TileSize size = best_tiles(a.r, a.np, 256, a.sum);
+    const TileSize size = best_tiles<OP>(a.r, a.np, 256, a.sum);
     if (size == kLarge)
         return start<OP, 256, 256, 64, 2, 4, 2>(a, rows, stream);
     if (size == kSquare)
         return start<OP, 128, 128, 64, 2, 2, 2>(a, rows, stream);
     if (size == kSmallSplit)
         return start<OP, 128, 64, 64, 3, 4, 1, 2>(a, rows, stream);
+    if constexpr (OP == kDgradKept) {
+        if (a.sum <= 512)
+            return start<OP, 128, 64, 64, 2, 4, 1>(a, rows, stream);
+    }
     return start<OP, 128, 64, 64, 3, 4, 1>(a, rows, stream);
 }
 

@@ -385,6 +385,32 @@ __device__ __forceinline__ void store_bf16(uint16_t *row, int c, int width, cons
     }
 }
 
+// The same by the packed hardware conversion (nearest even; on every float32
+// pattern the bits of f32_to_bf16, but that a NaN keeps its payload): an
+// instruction for two values in place of about ten. Forms that write much
+// beside short sums are bound by them (256 x 256 results a workgroup).
+__device__ __forceinline__ uint32_t pack2_hw(float a, float b)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
+template <int N>
+__device__ __forceinline__ void store_bf16_hw(uint16_t *row, int c, int width, const Cols<N> &o)
+{
+    if constexpr (N == 4) {
+        if (c < width)
+            *(u32x2 *)(row + c) = u32x2{pack2_hw(o.v[0], o.v[1]), pack2_hw(o.v[2], o.v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            if (c + i < width)
+                *(u32x4 *)(row + c + i) = u32x4{pack2_hw(o.v[i], o.v[i + 1]), pack2_hw(o.v[i + 2], o.v[i + 3]),
+                                                pack2_hw(o.v[i + 4], o.v[i + 5]), pack2_hw(o.v[i + 6], o.v[i + 7])};
+    }
+}
+
 // The same of a float32 row, written or added.
 template <int N>
 __device__ __forceinline__ void store_f32(float *row, int c, int width, const Cols<N> &o, bool add)

@@ -36,7 +36,9 @@ __device__ __forceinline__ float mxint8_step(uint32_t b)
 // The codes of 8 values of a block whose scale byte is b (the exponent field
 // of its largest magnitude; 255, an infinity or NaN: codes 0). The division by
 // a power of two is exact, and below 2^-126 what ldexp rounds is far below
-// half a step.
+// half a step. (One fma in place of ldexp and the addition needs a second way
+// for b below 7, whose registers cost the forward product more than it saves:
+// 1600 against 1577 us.)
 __device__ __forceinline__ u32x2 mxint8_codes(const float (&v)[8], uint32_t b)
 {
     uint32_t c[8];
