@@ -259,9 +259,10 @@ template <int OP, int TP, int TQ, int BK, int S, int WP, int WQ, int WK = 1> str
             // 1662 with two buffers of each and all copies in one half; five
             // buffers of 32 of the sum 2044).
             static_assert(S == 2 && BK == 64, "");
-            // int8: arithmetic may move between the rounds (32768 ragged rows, 16
-            // experts, 2 x 2048 x 7168: 800 us against 815; bf16 gains nothing)
-            constexpr int kMayCross = kI8 ? 0x6 : 0;
+            // arithmetic may move between the rounds where that is faster (32768
+            // ragged rows, 16 experts, 2 x 2048 x 7168: int8 800 us against 815,
+            // keeping 8 bits 1470 against 1500; the other forms gain nothing)
+            constexpr int kMayCross = kI8 || kKeep ? 0x6 : 0;
             constexpr int kReads = NI + NJ;
             // reads and copies before each of the NI rounds of NJ instructions
             // (transposing reads are twice as many, and spread further)
