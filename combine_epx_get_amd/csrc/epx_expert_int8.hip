@@ -9,6 +9,13 @@
 // whole numbers in 32 bits, exact up to the inner limit of epx.h, so neither
 // tiles nor groups of waves change a result; scales, activation and the 8-bit
 // form of the pre-activations are applied to them before the one rounding.
+//
+// Few rows an expert (256 rows over 8 experts of 2 x 2048 x 7168): the weights'
+// bytes, 43-44 us, 5.4 TB/s. Many (32768 ragged rows, 16 experts of 2 x 2048 x
+// 7168): 760-800 us, 2.4-2.5 POP/s; the matrix cores are 64 % busy, waves wait
+// 28 % of their time (a library product of one weight, without scales or
+// activation, took 875 us there and reached 2.46 POP/s at 8192^3). One row of
+// one expert: 7.4 us.
 #include "epx_expert_tiles.h"
 
 namespace epx {

@@ -13,6 +13,13 @@
 // instruction without another rounding. What comes to LDS is laid out as in
 // the bf16 weight gradient (rows of columns, 16-byte chunks permuted), so
 // fragments are read the same way.
+//
+// 32768 ragged rows on 16 experts: forward of 2 x 2048 x 7168 1430-1470 us, as
+// with bf16 pre-activations or a little less (half of their bytes are written);
+// input gradient of 7168 x 2048 850-900 us with the activation handed out, of
+// which writing takes about 100 and the epilogue's arithmetic as much; weight
+// gradient of 4096 x 7168 1650-1750 us, 1605-1650 from bf16 rows (converting
+// all rows by a call before, into 470 MB, takes 101 us).
 #include "epx_expert_tiles.h"
 
 namespace epx {

