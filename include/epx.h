@@ -591,7 +591,7 @@ EPX_API epx_status epx_expert_gemm_int8(const epx_expert_rows *rows, const int8_
  * activation in 8 bits in place of bf16: preact_codes int8 [num_rows, 2 *
  * width] and preact_scales uint8 [num_rows, 2 * width / 32], quantised from
  * the float32 sums as epx_mxint8_quantize does. out is that of
- * epx_expert_gemm. width is a multiple of 32, else sizes and alignment as
+ * epx_expert_gemm, whose float32 sums may be taken in another order. width is a multiple of 32, else sizes and alignment as
  * there; preact_codes is 16-byte aligned. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_keep8(const epx_expert_rows *rows, const void *x, const void *w,
                                          int32_t width, int32_t inner, int8_t *preact_codes,
@@ -612,8 +612,8 @@ EPX_API epx_status epx_expert_gemm_dgrad_kept8(const epx_expert_rows *rows, cons
 
 /* epx_expert_gemm_wgrad for rows x kept in 8 bits: x_codes int8 [num_rows,
  * inner], x_scales uint8 [num_rows, inner / 32], as epx_mxint8_quantize
- * writes them. dw is that of epx_expert_gemm_wgrad on the values kept. inner is
- * a multiple of 32. Errors: EPX_ERR_ARG. */
+ * writes them. dw is that of epx_expert_gemm_wgrad on the values kept, whose
+ * float32 sums may be taken in another order. inner is a multiple of 32. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_wgrad_kept8(const epx_expert_rows *rows, const void *dy,
                                                const int8_t *x_codes, const uint8_t *x_scales,
                                                int32_t width, int32_t inner, int32_t dw_dtype,

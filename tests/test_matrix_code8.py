@@ -31,3 +31,29 @@ def test_waits_around_assembly_statements(source):
     print(f"{source}: {kernels} kernels, {copies} copies, {products} matrix instructions in statements")
     assert kernels >= 15 and copies >= 200 and products >= 100
     assert not bad, bad
+
+
+def test_the_large_weight_gradient_waits_for_its_copies():
+    """Its waits allow as many memory operations to be under way as loads of codes and scale bytes follow its last
+    copies: at least that many have to stand between the two, or the wait would not reach the copies."""
+    r = subprocess.run([build.HIPCC, *build.FLAGS, "-w", "--cuda-device-only", "-S",
+                        os.path.join(build.CSRC, "epx_expert_kept8.hip"), "-o", "-"], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr
+    memory = ("buffer_", "global_", "flat_", "scratch_")
+    checked = 0
+    for name, blocks in functions(r.stdout):
+        if "wgrad_kept_deep" not in name:
+            continue
+        for _, code in blocks:
+            for at, (op, operands, inside) in enumerate(code):
+                if not (inside and op == "s_waitcnt" and "vmcnt(4)" in " ".join(operands)):
+                    continue
+                loads = 0
+                for before in reversed(code[:at]):
+                    if before[0].startswith(memory):
+                        if before[2]:
+                            break
+                        loads += 1
+                assert loads >= 4, (name, at, loads)
+                checked += 1
+    assert checked >= 4   # before the loop and in it, for either type of result
