@@ -365,11 +365,15 @@ template <bool F32> hipError_t start_kept_deep(Args8 a, hipStream_t stream)
 
 // Tiles (columns x by columns dy) by measured times, us: 64 x 64 with eight
 // waves that divide the sum / 64 x 128 with four pairs that do / 128 x 128 with
-// two groups that do / 128 x 128, four a CU / 256 x 256. Few tiles, and a step
-// of the sum at least for each wave: 2 experts of 376 x 640, 5200 rows each 25 /
+// two groups that do / 128 x 128, four a CU / 256 x 256. Few tiles, and for
+// those of 64 a step of the sum at least for each wave: 2 experts of 376 x 640, 5200 rows each 25 /
 // 51 / 63 / 104 / 121 (with four waves in place of eight 37); 1 of 1024 x 1024,
 // 20000 rows 81 / 165 / 220 / 375 / 431; 4 of 512 x 512, 512 rows 7.7 / 8.2 / 10.7
-// / 11.9 / 22; 4 of 512 x 1024, 256 rows 12.0 / 7.6 / 8.8 / 9.1 / 16.7, 4096 rows
+// / 11.9 / 22; smaller still where that gives more workgroups, 32 x 32 / 32 x 64 /
+// 64 x 64: 1 of 328 x 608, 14922 rows (209 tiles of 32 x 32) 49 / 58 / 59; 1 of 512 x
+// 512, 1000 rows (256) 5.8 / 6.1 / 8.0; 1 of 128 x 128, 40000 rows (16) 94 / 103 /
+// 138; 1 of 256 x 2048, 8192 rows (256 of 32 x 64) 48 / 30 / 40; 1 of 512 x 512, 32 rows 4.2 / 4.6 / 5.8; 2 of 376 x 640, 5200
+// rows (240) 34 / 23.4 / 24.7; 4 of 512 x 1024, 256 rows 12.0 / 7.6 / 8.8 / 9.1 / 16.7, 4096 rows
 // 39 / 40 / 51 / 81 / 96; but 8 of 256 x 256, 32 rows 6.1 / 5.9 / 7.3 / 5.0 / 12.8.
 // Else the last three, by the rounds of workgroups and a round's time, about
 // linear in the rows of an expert: 2 of 4624 x 352, 11246 rows 137 / 218 / 249; 8
@@ -383,6 +387,10 @@ template <bool F32> hipError_t start_wgrad_kept(const Args8 &a, hipStream_t stre
         return (int64_t)((a.np + p - 1) / p) * ((a.nq + q - 1) / q) * a.r.n;
     };
     const int64_t sum = a.r.num_rows / a.r.n, squares = tiles(128, 128);
+    if (tiles(32, 32) <= 256)
+        return start_kept<F32, 32, 32, 32, 1, 1, 8>(a, stream);
+    if (tiles(32, 64) <= 256)
+        return start_kept<F32, 32, 64, 32, 1, 1, 8>(a, stream);
     if (sum >= 256 && tiles(64, 64) <= 256)
         return start_kept<F32, 64, 64, 32, 1, 1, 8>(a, stream);
     if (sum >= 256 && tiles(64, 128) <= 256)

@@ -37,6 +37,9 @@ MORE = [
     ("uneven blocks", [70, 0, 3], 1, None, 96, 160),
     ("decode of one expert's size", [32] * 8, 0, None, 1024, 2048),
     ("long sum, few rows", [1, 2], 0, None, 64, 8192),
+    ("one small matrix, many rows", [3001], 2, None, 136, 256),
+    ("two matrices of a few tiles", [700, 0, 529], 1, [2, 0, 1], 376, 640),
+    ("a matrix of more tiles", [1300], 0, None, 1024, 992),
 ]
 CASES = BF16_CASES + MORE
 
