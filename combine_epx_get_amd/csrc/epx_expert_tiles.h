@@ -720,9 +720,9 @@ bool start_split(const A &a, int64_t rows, hipStream_t stream, hipError_t &statu
 enum TileSize { kLarge, kSquare, kSmall, kSmallSplit };
 // A round's time for each, ns: a start and its growth with the sum (in 80ths).
 struct TileCosts {
-    int64_t large, large_sum, square, square_sum, small, small_sum, small_slots;
+    int64_t large, large_sum, square, square_sum, small, small_sum;
 };
-constexpr TileCosts kCosts = {9000, 1880, 4500, 1320, 4200, 1008, 512};
+constexpr TileCosts kCosts = {9000, 1880, 4500, 1320, 4200, 1008};
 // Forms in 8 bits, whose small tiles have two buffers for sums up to 1280 (of
 // bf16 values, or of pairs of int8), three a CU: one writes while others
 // multiply. us, large / square / small with three buffers / with two. Forward,
@@ -733,7 +733,7 @@ constexpr TileCosts kCosts = {9000, 1880, 4500, 1320, 4200, 1008, 512};
 // of 2048, 2048 x 64 84 / 85 / 132 / 97, x 512 115 / 122 / 176 / 141, x 2048 270 /
 // 332 / 414 / 405; 13 of 461, 1280 x 240 13.7 / 13.9 / 14.7 / 12.3; 2 of 1337, 1408 x
 // 6512 75 / 70 / 98 / 103; 16 of 96, 2048 x 7168 95 / 100 / 125 / 137.
-constexpr TileCosts kCosts8 = {9500, 1520, 4800, 1040, 3900, 1000, 768};
+constexpr TileCosts kCosts8 = {9500, 1520, 4800, 1040, 3900, 1000};
 // The gradient through kept pre-activations, which writes both gradients and
 // the activation, from codes, at about 170 cycles a result of a wave. As above:
 // 16 experts of 2048 rows, 64 x 2048 185 / 173 / 186 / 162, 256 x 2048 192 / 216 /
@@ -741,7 +741,17 @@ constexpr TileCosts kCosts8 = {9500, 1520, 4800, 1040, 3900, 1000, 768};
 // 4632, 192 x 1088 30.9 / 19.7 / 18.1 / 16.5; 4 of 1000, 512 x 1088 36 / 23.6 / 23.0
 // / 20.5; 2 of 8000, 320 x 640 35 / 31.6 / 31.0 / 27.8; 37 of 92, 88 x 992 15.9 /
 // 15.9 / 15.6 / 13.5; but 24 of 83, 1048 x 544 24 / 22 / 15.0 / 17.2 (above 512 three).
-constexpr TileCosts kCostsKept = {36000, 1424, 18000, 1440, 13700, 1304, 768};
+constexpr TileCosts kCostsKept = {36000, 1424, 18000, 1440, 13700, 1304};
+
+// Two buffers for a small tile of the forms in 8 bits (from 64 rows an expert):
+// three workgroups a CU in place of two, so a round of them is 768 tiles in
+// place of 512. (At 513 to 768 tiles of three buffers, square / small, us, ragged
+// rows: forward, kept, 9 experts of 894 rows, 224 x 2760 46.8 / 63.5; int8 gated
+// 52 of 70, 576 x 2592 33.9 / 46.4; gradient 27 of 127, 1056 x 3360 65.1 / 83.3.)
+template <int OP> bool two_buffers(int64_t sum)
+{
+    return OP >= kForwardKeep && sum <= (OP == kDgradKept ? 512 : 1280);
+}
 
 template <int OP> TileSize best_tiles(const ExpertRows &r, int32_t columns, int columns_of_256, int64_t sum)
 {
@@ -751,7 +761,7 @@ template <int OP> TileSize best_tiles(const ExpertRows &r, int32_t columns, int 
     };
     const int64_t large = rounds(256, 256, 256) * (c.large + sum * c.large_sum / 80);
     const int64_t square = rounds(128, 128, 512) * (c.square + sum * c.square_sum / 80);
-    const int64_t small = rounds(64, 128, c.small_slots) * (c.small + sum * c.small_sum / 80);
+    const int64_t small = rounds(64, 128, two_buffers<OP>(sum) ? 768 : 512) * (c.small + sum * c.small_sum / 80);
     if (large <= square && large <= small)
         return kLarge;
     if (square <= small)
@@ -792,7 +802,7 @@ template <int OP, typename A> hipError_t start_forward(const A &a, hipStream_t s
         // two buffers as said above; sums of few rows an expert, which wait for
         // the weights, up to half as long (int8, 64 of 16 rows, 1024 x 2048 42.0 with
         // three buffers, 45.2 with two; 42 of 20, 416 x 592 6.8 with four, 6.2 with two)
-        if (wide && a.sum <= (rows > 64 * n ? 1280 : 640))
+        if (wide && (rows > 64 * n ? two_buffers<OP>(a.sum) : a.sum <= 640))
             return start<OP, 128, 64, 64, 2, P, Q>(a, rows, stream);
         if (!wide && a.sum <= 640)
             return start<OP, 128, 32, 64, 2, P, Q>(a, rows, stream);
@@ -816,7 +826,7 @@ template <int OP, typename A> hipError_t start_dgrad(const A &a, hipStream_t str
     if (size == kSmallSplit)
         return start<OP, 128, 64, 64, 3, 4, 1, 2>(a, rows, stream);
     if constexpr (OP == kDgradKept) {
-        if (a.sum <= 512)
+        if (two_buffers<OP>(a.sum))
             return start<OP, 128, 64, 64, 2, 4, 1>(a, rows, stream);
     }
     return start<OP, 128, 64, 64, 3, 4, 1>(a, rows, stream);
