@@ -1,7 +1,12 @@
 """Which tiles the experts' products on 8-bit rows take, by the kernels that
 the library's own host code launches (no GPU)."""
+import re
+
 import pytest
 
+from tests import experts_reference as ref
+from tests import test_expert_tiles8_gpu as tiles
+from tests import test_experts8_gpu as products
 from tests.launches import Recorder, expert_calls
 
 
@@ -35,3 +40,33 @@ def test_a_round_of_small_tiles_with_three_buffers_is_512(recorder, call, rows, 
 @pytest.mark.parametrize("call,rows,experts,width,inner", SHORT)
 def test_a_round_of_small_tiles_with_two_buffers_is_768(recorder, call, rows, experts, width, inner):
     assert recorder.launched(expert_calls(rows, experts, width, inner)[call]) == [small(call, 2)]
+
+
+# call: (its template argument, units of width and inner)
+CALLS = {"int8": (7, (8, 16)), "int8 gated": (8, (8, 16)), "int8 kept": (9, (32, 16)), "keep8": (6, (32, 8)), "dgrad8": (10, (8, 32)),
+         "wgrad8 bf16": ("false", (8, 32)), "wgrad8 f32": ("true", (8, 32))}
+
+
+def launched(recorder, call, case):
+    name, cnt, gap, order, width, inner = case
+    width, inner = (products.up(v, u) for v, u in zip((width, inner), CALLS[call][1]))
+    return recorder.launched(expert_calls(ref.ranges(cnt, gap, order)[1], len(cnt), width, inner)[call])
+
+
+def tile_cases(call):
+    return tiles.CASES[call.removesuffix(" bf16").removesuffix(" f32")]
+
+
+def test_every_tile_has_a_case_with_results(recorder):
+    """Each kernel of these calls is launched by a case that the GPU tests hold against 64-bit products."""
+    reached = {k for call in CALLS for case in products.CASES + [c for _, c in tile_cases(call)]
+               for k in launched(recorder, call, case)}
+    kernels = {k for k in recorder.kernels() if re.match(r"gemm_kernel<(6|7|8|9|10),|wgrad_kept", k)}
+    assert len(kernels) >= 50 and kernels == reached, sorted(kernels ^ reached)
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_cases_take_the_tiles_that_they_are_for(recorder, call):
+    kernel = "wgrad_kept_kernel" if "wgrad" in call else "gemm_kernel"
+    for tile, case in tile_cases(call):
+        assert launched(recorder, call, case) == [f"{kernel}<{CALLS[call][0]}, {tile}>"], case[0]
