@@ -591,8 +591,9 @@ EPX_API epx_status epx_expert_gemm_int8(const epx_expert_rows *rows, const int8_
  * activation in 8 bits in place of bf16: preact_codes int8 [num_rows, 2 *
  * width] and preact_scales uint8 [num_rows, 2 * width / 32], quantised from
  * the float32 sums as epx_mxint8_quantize does. out is that of
- * epx_expert_gemm, whose float32 sums may be taken in another order. width is a multiple of 32, else sizes and alignment as
- * there; preact_codes is 16-byte aligned. Errors: EPX_ERR_ARG. */
+ * epx_expert_gemm, whose float32 sums may be taken in another order. width is a
+ * multiple of 32, else sizes and alignment as there; preact_codes is 16-byte
+ * aligned. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_keep8(const epx_expert_rows *rows, const void *x, const void *w,
                                          int32_t width, int32_t inner, int8_t *preact_codes,
                                          uint8_t *preact_scales, void *out, void *stream);
@@ -602,8 +603,9 @@ EPX_API epx_status epx_expert_gemm_keep8(const epx_expert_rows *rows, const void
  * [num_rows, 2 * inner / 32].
  *  act_out  NULL, or bf16 [num_rows, inner]: silu(gate) * up of the kept
  *           values, the product's input again, for the weights' gradient
- * inner is a multiple of 32; act_out and preact_codes are 16-byte aligned.
- * Errors: EPX_ERR_ARG. */
+ * dx is that of epx_expert_gemm_dgrad on the values kept, whose float32 sums may
+ * be taken in another order. inner is a multiple of 32; act_out and preact_codes
+ * are 16-byte aligned. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_dgrad_kept8(const epx_expert_rows *rows, const void *dy,
                                                const void *w, int32_t width, int32_t inner,
                                                const int8_t *preact_codes,
@@ -613,7 +615,10 @@ EPX_API epx_status epx_expert_gemm_dgrad_kept8(const epx_expert_rows *rows, cons
 /* epx_expert_gemm_wgrad for rows x kept in 8 bits: x_codes int8 [num_rows,
  * inner], x_scales uint8 [num_rows, inner / 32], as epx_mxint8_quantize
  * writes them. dw is that of epx_expert_gemm_wgrad on the values kept, whose
- * float32 sums may be taken in another order. inner is a multiple of 32. Errors: EPX_ERR_ARG. */
+ * float32 sums may be taken in another order. It needs no rows in bf16 (33/64 of
+ * their memory), but is no faster than epx_mxint8_dequantize and
+ * epx_expert_gemm_wgrad, and slower for large float32 gradients. inner is a
+ * multiple of 32. Errors: EPX_ERR_ARG. */
 EPX_API epx_status epx_expert_gemm_wgrad_kept8(const epx_expert_rows *rows, const void *dy,
                                                const int8_t *x_codes, const uint8_t *x_scales,
                                                int32_t width, int32_t inner, int32_t dw_dtype,
