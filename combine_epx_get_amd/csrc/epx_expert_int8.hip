@@ -11,11 +11,14 @@
 // form of the pre-activations are applied to them before the one rounding.
 //
 // Few rows an expert (256 rows over 8 experts of 2 x 2048 x 7168): the weights'
-// bytes, 43-44 us, 5.4 TB/s. Many (32768 ragged rows, 16 experts of 2 x 2048 x
-// 7168): 760-800 us, 2.4-2.5 POP/s; the matrix cores are 64 % busy, waves wait
-// 28 % of their time (a library product of one weight, without scales or
-// activation, took 875 us there and reached 2.46 POP/s at 8192^3). One row of
-// one expert: 7.4 us.
+// bytes, 43-44 us, 5.4 TB/s, and 45.5 with the pre-activations kept. Many (32768
+// ragged rows, 16 experts of 2 x 2048 x 7168): 760-820 us, 2.3-2.5 POP/s; the
+// matrix cores are 64 % busy, waves wait 28 % of their time (a library product of
+// one weight, without scales or activation, took 860-875 us there and reached 2.46
+// POP/s at 8192^3); 829-835 kept. The second product, without activation: 8 of
+// 7168 x 2048, 256 rows 27 us, 4.4 TB/s of weights; 16 of them, 32768 rows 485-490
+// us, 2.0 POP/s: half as many steps a tile beside the same results. One row of one
+// expert: 7.4 us.
 #include "epx_expert_tiles.h"
 
 namespace epx {

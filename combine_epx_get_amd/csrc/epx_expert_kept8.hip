@@ -14,12 +14,14 @@
 // the bf16 weight gradient (rows of columns, 16-byte chunks permuted), so
 // fragments are read the same way.
 //
-// 32768 ragged rows on 16 experts: forward of 2 x 2048 x 7168 1430-1470 us, as
+// 32768 ragged rows on 16 experts: forward of 2 x 2048 x 7168 1430-1550 us, as
 // with bf16 pre-activations or a little less (half of their bytes are written);
-// input gradient of 7168 x 2048 850-900 us with the activation handed out, of
-// which writing takes about 100 and the epilogue's arithmetic as much; weight
-// gradient of 4096 x 7168 1650-1750 us, 1605-1650 from bf16 rows (converting
-// all rows by a call before, into 470 MB, takes 101 us).
+// input gradient of 7168 x 2048 850-920 us with the activation handed out (35 of
+// them for it), of which writing takes about 100 and the epilogue's arithmetic as
+// much; weight gradient of 4096 x 7168 1650-1810 us, 1605-1650 from bf16 rows.
+// Converting all rows by a call before takes 101 us and 470 MB: what the weight
+// gradient from kept rows saves is that memory, and no time (side by side 1746
+// and 1741 us; float32 results 1990 and 1849, added to what is there 2350).
 #include "epx_expert_tiles.h"
 
 namespace epx {
@@ -76,10 +78,14 @@ template <int TP, int BK, int LANES> struct Stage {
 };
 
 // P = x (codes), Q = dy. WP x WQ waves compute a tile, WK groups of them take
-// every WK-th step each, a step ahead of what they multiply. (Copies of codes
-// and scale bytes to LDS, three steps ahead, and from there through registers
-// took longer at every size: what bounds these tiles is the instructions of the
-// conversion, not the memory's latency.)
+// every WK-th step each, a step ahead of what they multiply. (Tiles of 64 x 64
+// and more are bound by the instructions of the conversion: copies of codes and
+// scale bytes to LDS, three steps ahead, and from there through registers took
+// longer at every size of theirs. Those of 32 columns are bound by the memory's
+// latency: a step has 4 or 8 matrix instructions, and a wave one step under way.
+// 1 expert of 328 x 608, 14922 rows: 58 steps a wave in 48 us, of which waves
+// wait 65 %; 1 of 128 x 128, 40000 rows, 16 tiles on 256 CUs: 89 us, 58 %. More
+// steps under way are not tried for them.)
 template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK> struct KeptKernel {
     using Base = Kernel<F32 ? kWgradKeptF32 : kWgradKept, TP, TQ, BK, 2, WP, WQ, WK>;
     static constexpr int kWaves = WP * WQ, kLanes = kWaves * kWave;
@@ -195,6 +201,12 @@ template <bool F32, int TP, int TQ, int BK, int WP, int WQ, int WK> struct KeptK
 // the halves, orders all of it: what was read before it is free after it, what
 // was written or copied before it is there. (Whole sets of dy's fragments, as
 // the bf16 kernel holds them, would leave no registers for the codes.)
+//
+// The third buffer is there because this step's dy and the next one's are both
+// read in the second half; it does not keep dy's copies under way for a step.
+// The waits that the compiler puts before the conversions count its own loads
+// alone, so they take in the copies, which went out after those: a step's dy has
+// arrived half a step later, before the meeting's own wait for it.
 template <bool F32> struct KeptDeep {
     static constexpr int TP = 256, TQ = 256, BK = 64, WP = 4, WQ = 2;
     using Base = Kernel<F32 ? kWgradKeptF32 : kWgradKept, TP, TQ, BK, 2, WP, WQ>;
@@ -363,7 +375,8 @@ template <bool F32> hipError_t start_kept_deep(Args8 a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Tiles (columns x by columns dy) by measured times, us: 64 x 64 with eight
+// Tiles (columns x by columns dy) by measured times, us (of bf16 results, but for
+// 1 of 256 x 2048 and 8 of 256 x 256, float32): 64 x 64 with eight
 // waves that divide the sum / 64 x 128 with four pairs that do / 128 x 128 with
 // two groups that do / 128 x 128, four a CU / 256 x 256. Few tiles, and for
 // those of 64 a step of the sum at least for each wave: 2 experts of 376 x 640, 5200 rows each 25 /
@@ -381,6 +394,11 @@ template <bool F32> hipError_t start_kept_deep(Args8 a, hipStream_t stream)
 // 11.0 / 15.7; 2 of 1408 x 2912, 647 rows 30 / 24 / 28; 16 of 2048 x 7168, 64 rows
 // 362 / 159 / 174, 256 rows 464 / 265 / 258, 1024 rows 973 / 648 / 526; 64 of 1024 x
 // 2048, 64 rows 202 / 77 / 100; 1 of 4096 x 4096, 2048 rows 117 / 85 / 66.
+// Float32 results take the same rule, though they write twice the bytes: over 62
+// drawn sizes it takes 2 % longer than the best of the seven tiles for bf16, 3 %
+// for float32 and 4 % for float32 added. It is furthest off where a large tile
+// has a short sum: 30 experts of 371 rows, 1768 x 320, 256 x 256 / 128 x 128, bf16
+// 38 / 30, float32 47 / 33, added 60 / 44.
 template <bool F32> hipError_t start_wgrad_kept(const Args8 &a, hipStream_t stream)
 {
     const auto tiles = [&](int p, int q) {
